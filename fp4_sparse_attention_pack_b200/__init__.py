@@ -17,13 +17,16 @@ __all__ = ["Csa2Error", "lib", "csa2_cache", "csa2_window", "csa2_model", "csa2_
            "index_topk_pool", "index_topk_in_pool", "POOL_BLOCK", "MAX_POOL_BLOCKS", "WIN_BF16", "WIN_FP8",
            "sparse_attn",
            "sparse_attn_workspace", "window_append", "layer_step", "layer_step_workspace", "layer_step_launches", "seq_image_bytes", "cache_export",
-           "cache_import",
-           "SWA_ONLY", "FULL", "REINDEX", "REUSE", "DTYPE_BF16", "DTYPE_F32"]
+           "cache_import", "csa2_heads", "csa2_rotary", "csa2_kv_cache", "rotary", "rotate", "kv_cache", "kv_append",
+           "kv_attn", "kv_attn_workspace", "KV_BF16", "KV_F16", "KV_E4M3",
+           "SWA_ONLY", "FULL", "REINDEX", "REUSE", "DTYPE_BF16", "DTYPE_F32", "DTYPE_F16"]
 
 SWA_ONLY, FULL, REINDEX, REUSE = 0, 1, 2, 3
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
 POOL_BLOCK, MAX_POOL_BLOCKS = 8, 8192
 WIN_BF16, WIN_FP8 = 0, 1
+KV_BF16, KV_F16, KV_E4M3 = 0, 1, 2
+MAX_ROT = 256
 DEVERR_CAPACITY, DEVERR_PAGE, DEVERR_COUNT, DEVERR_TIMEOUT, DEVERR_IMAGE = 1, 2, 4, 8, 16
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -64,6 +67,21 @@ class csa2_step_out(ctypes.Structure):
     _fields_ = [("out", ctypes.POINTER(_vp)), ("idx", ctypes.POINTER(_vp))]
 
 
+class csa2_heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class csa2_rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", _vp), ("axis", ctypes.POINTER(ctypes.c_uint8)), ("rot_dim", _i32),
+                ("rot_offset", _i32), ("neighbours", _i32), ("n_axes", _i32)]
+
+
+class csa2_kv_cache(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("page_table", _vp), ("n_tokens", _vp), ("status", _vp),
+                ("batch", _i32), ("max_pages", _i32), ("num_pages", _i32), ("kv_heads", _i32),
+                ("head_dim", _i32), ("dtype", _i32)]
+
+
 _lib = None
 
 
@@ -98,6 +116,14 @@ def lib():
             ("csa2_seq_image_bytes", _sz, [ctypes.c_int]),
             ("csa2_cache_export", ctypes.c_int, [P(csa2_cache), ctypes.c_int, _vp, ctypes.c_int, _vp]),
             ("csa2_cache_import", ctypes.c_int, [P(csa2_cache), ctypes.c_int, _vp, ctypes.c_int, _vp]),
+            ("csa2_rotate", ctypes.c_int, [P(csa2_rotary), P(csa2_heads), P(csa2_heads), ctypes.c_int,
+                                           ctypes.c_int64, ctypes.c_int, ctypes.c_int, _vp, ctypes.c_int, _vp]),
+            ("csa2_kv_append", ctypes.c_int, [P(csa2_kv_cache), P(csa2_heads), P(csa2_heads), ctypes.c_int, _vp,
+                                              ctypes.c_int, ctypes.c_int, _vp, P(csa2_rotary), _vp, _vp]),
+            ("csa2_kv_attn_workspace", _sz, [P(csa2_kv_cache), ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+            ("csa2_kv_attn", ctypes.c_int, [P(csa2_kv_cache), P(csa2_heads), ctypes.c_int, ctypes.c_int, _vp,
+                                            ctypes.c_int, ctypes.c_int, _f32, ctypes.c_int, P(csa2_heads), _vp,
+                                            _vp, _sz, _vp]),
         ]:
             f = getattr(L, name)
             f.restype = res
@@ -235,3 +261,143 @@ def index_topk_noalloc(cache: csa2_cache, q_idx, w, K: int, idx_out, score_out=N
     H_idx = q_idx.shape[1]
     _ok(f(ctypes.byref(cache), _ptr(q_idx), _ptr(w), H_idx, K, _ptr(idx_out), _ptr(score_out),
           _stream(stream)), "csa2_index_topk_noalloc")
+
+
+# ---------------------------------------------------------------- paged key/value cache
+
+def _code(t, codes, what):
+    """The library's code of t's dtype, from (torch name, code) pairs."""
+    for name, code in codes:
+        if str(t.dtype) == name:
+            return code
+    raise ValueError(f"{what}: {t.dtype} is not supported")
+
+
+_HEAD_TYPES = (("torch.bfloat16", DTYPE_BF16), ("torch.float16", DTYPE_F16), ("torch.float32", DTYPE_F32))
+_KV_TYPES = (("torch.bfloat16", KV_BF16), ("torch.float16", KV_F16), ("torch.float8_e4m3fn", KV_E4M3))
+
+
+def _want(t, what, dtype, shape, device=None):
+    """A contiguous CUDA tensor of this dtype and shape (the library sees only its address)."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} is on {t.device}, not on the call's CUDA device")
+    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+
+
+def _heads(t, what, shape=None, like=None):
+    """csa2_heads of a [tokens][heads][channels] tensor with contiguous channels."""
+    if not t.is_cuda or (like is not None and (t.device != like.device or t.dtype != like.dtype)):
+        raise ValueError(f"{what} is {t.dtype} on {t.device}: it must be of the call's type and on its CUDA device")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must have shape {tuple(shape) if shape else '[tokens][heads][channels]'}, "
+                         f"not {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what}: the channels must be contiguous")
+    return csa2_heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _same_device(cache, t, what):
+    pages = getattr(cache, "_keep", (None,))[0]
+    if pages is not None and pages.device != t.device:
+        raise ValueError(f"{what} is on {t.device}, the cache on {pages.device}")
+
+
+class _on:
+    """The device of a tensor as the current one during a call, and its stream."""
+
+    def __init__(self, t, stream):
+        import torch
+        self.guard = torch.cuda.device(t.device)
+        self.device, self.stream = t.device, stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *e):
+        return self.guard.__exit__(*e)
+
+
+def rotary(inv_freq, rot_dim: int, offset: int = 0, neighbours: bool = False, n_axes: int = 1, axis=None) -> csa2_rotary:
+    """A rotation: channels offset .. offset + rot_dim - 1 of a head turn in pairs (neighbours, or half the
+    rotation apart) by position * inv_freq[pair] (fp32 CUDA tensor).  axis (a list, one entry per pair) says
+    which of the n_axes positions turns it."""
+    _want(inv_freq, "inv_freq", "torch.float32", (rot_dim // 2,))
+    r = csa2_rotary(inv_freq.data_ptr(), None, rot_dim, offset, int(neighbours), n_axes)
+    if axis is not None:
+        if len(axis) != rot_dim // 2:
+            raise ValueError(f"axis has {len(axis)} entries, not one for each of the {rot_dim // 2} pairs")
+        r.axis = (ctypes.c_uint8 * len(axis))(*axis)
+    r._keep = inv_freq  # the descriptor holds its address
+    return r
+
+
+def rotate(rot: csa2_rotary, x, pos, out, inverse: bool = False, stream=None):
+    """out = x [tokens][heads][channels] rotated at pos int32 [n_axes][tokens] (out may be x); inverse turns back."""
+    xd = _heads(x, "x")
+    yd = _heads(out, "out", x.shape, x)
+    _want(pos, "pos", "torch.int32", (rot.n_axes, x.shape[0]), x.device)
+    with _on(x, stream) as s:
+        _ok(lib().csa2_rotate(ctypes.byref(rot), ctypes.byref(xd), ctypes.byref(yd), _code(x, _HEAD_TYPES, "x"),
+                              x.shape[0], x.shape[1], x.shape[2], pos.data_ptr(), int(inverse), s), "csa2_rotate")
+
+
+def kv_cache(k_pages, v_pages, page_table, n_tokens, status) -> csa2_kv_cache:
+    """Descriptor of a paged key/value cache: pools [pages][kv_heads][64][head_dim] (bf16, fp16 or float8_e4m3fn),
+    page_table int32 [batch][max_pages], n_tokens int32 [batch], status int32 (one word or more)."""
+    pages, heads, rows, dim = k_pages.shape
+    if rows != 64:
+        raise ValueError(f"a page has 64 rows, not {rows}")
+    _want(k_pages, "k_pages", str(k_pages.dtype), k_pages.shape)
+    _want(v_pages, "v_pages", str(k_pages.dtype), k_pages.shape, k_pages.device)
+    batch, max_pages = page_table.shape
+    _want(page_table, "page_table", "torch.int32", (batch, max_pages), k_pages.device)
+    _want(n_tokens, "n_tokens", "torch.int32", (batch,), k_pages.device)
+    if not status.is_cuda or status.element_size() != 4 or status.numel() < 1:
+        raise ValueError("status must be a CUDA tensor of 32-bit words")
+    c = csa2_kv_cache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), n_tokens.data_ptr(),
+                      status.data_ptr(), batch, max_pages, pages, heads, dim, _code(k_pages, _KV_TYPES, "k_pages"))
+    c._keep = (k_pages, v_pages, page_table, n_tokens, status)  # the descriptor holds their addresses
+    return c
+
+
+def kv_append(cache: csa2_kv_cache, k, v, cu, max_new: int, start=None, rotary=None, pos=None, stream=None):
+    """Write the new tokens k, v [total][kv_heads][head_dim] (sequence b: rows cu[b] .. cu[b + 1] - 1) behind
+    start (int32 [batch]; None: behind the tokens held), the keys rotated at pos int32 [n_axes][total]
+    (None: their slots)."""
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    kd, vd = _heads(k, "k", shape), _heads(v, "v", shape, k)
+    _same_device(cache, k, "k")
+    _want(cu, "cu", "torch.int32", (cache.batch + 1,), k.device)
+    if start is not None:
+        _want(start, "start", "torch.int32", (cache.batch,), k.device)
+    if pos is not None:
+        _want(pos, "pos", "torch.int32", (rotary.n_axes if rotary is not None else 0, k.shape[0]), k.device)
+    with _on(k, stream) as s:
+        _ok(lib().csa2_kv_append(ctypes.byref(cache), ctypes.byref(kd), ctypes.byref(vd), _code(k, _HEAD_TYPES, "k"),
+                                 cu.data_ptr(), k.shape[0], max_new, _ptr(start),
+                                 ctypes.byref(rotary) if rotary is not None else None, _ptr(pos), s),
+            "csa2_kv_append")
+
+
+def kv_attn_workspace(cache: csa2_kv_cache, total: int, max_new: int, H: int) -> int:
+    return int(lib().csa2_kv_attn_workspace(ctypes.byref(cache), total, max_new, H))
+
+
+def kv_attn(cache: csa2_kv_cache, q, cu, max_new: int, scale: float, out, ws, lse=None, window: int = 0, stream=None):
+    """out [total][H][head_dim] = attention of the new tokens' queries q over the cache (their own keys appended
+    before); lse fp32 [total][H] (optional); window > 0: each token sees its last `window` keys only."""
+    qd = _heads(q, "q", (q.shape[0], q.shape[1], cache.head_dim))
+    od = _heads(out, "out", q.shape, q)
+    _same_device(cache, q, "q")
+    if ws is not None and ws.device != q.device:
+        raise ValueError(f"ws is on {ws.device}, not on the call's CUDA device")
+    _want(cu, "cu", "torch.int32", (cache.batch + 1,), q.device)
+    if lse is not None:
+        _want(lse, "lse", "torch.float32", q.shape[:2], q.device)
+    with _on(q, stream) as s:
+        _ok(lib().csa2_kv_attn(ctypes.byref(cache), ctypes.byref(qd), q.shape[1], _code(q, _HEAD_TYPES, "q"),
+                               cu.data_ptr(), q.shape[0], max_new, float(scale), window, ctypes.byref(od), _ptr(lse),
+                               _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0, s), "csa2_kv_attn")

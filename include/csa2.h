@@ -19,6 +19,15 @@
  *   csa2_layer_step   one decode step of a whole stack of layers under the
  *                     static Full / Reindex / Reuse mode table.
  *
+ * Beside them stand the operators of an ordinary paged key/value cache, for the
+ * layers and steps of the same serving program that CSA2 does not cover (layers
+ * with full attention or a wide window, a draft model, chunks of a prompt):
+ *
+ *   csa2_rotate       rotary positions with one to three axes, and the inverse;
+ *   csa2_kv_append    new keys and values to the pages, rotated on the way;
+ *   csa2_kv_attn      attention of a chunk of new tokens (from one to
+ *                     thousands) over the pages.
+ *
  * Conventions (all entry points):
  *   - Every tensor is caller-owned DEVICE memory unless stated otherwise; the
  *     library allocates nothing and keeps no pointer after a call returns.
@@ -84,7 +93,7 @@ typedef enum {
     CSA2_MODE_REUSE = 3     /* reuses cache, keys and Top-K indices */
 } csa2_mode;
 
-typedef enum { CSA2_DTYPE_BF16 = 0, CSA2_DTYPE_F32 = 1 } csa2_dtype;
+typedef enum { CSA2_DTYPE_BF16 = 0, CSA2_DTYPE_F32 = 1, CSA2_DTYPE_F16 = 2 } csa2_dtype;
 
 /* Sticky device error bits (csa2_cache.status). */
 #define CSA2_DEVERR_CAPACITY 0x1u /* an append would exceed max_pages * 64 entries */
@@ -481,6 +490,143 @@ int csa2_cache_import(const csa2_cache* cache, int seq, const void* image, int c
  * model table is invalid or `in` is NULL.  Enqueues nothing.
  */
 int csa2_layer_step_launches(const csa2_model* model, const csa2_step_in* in);
+
+/*
+ * Operators of an ordinary paged key/value cache.  (The pages have no
+ * counterpart: they cover the compressed cache only.  Formulas and conventions
+ * are this library's own.)
+ *
+ * A tensor of heads: element (token t, head h, channel c) is at
+ * data[t * token_stride + h * head_stride + c] (strides in elements; channels
+ * contiguous).  data is 16-byte aligned and the strides are multiples of 8
+ * elements (CSA2_ERR_ALIGN).  Strides are not negative; those of an output
+ * keep its rows apart (each is at least the row's channels where it counts).
+ */
+typedef struct {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} csa2_heads;
+
+/*
+ * Rotary positions.  Channels rot_offset .. rot_offset + rot_dim - 1 of a head
+ * form rot_dim / 2 pairs: pair i is channels (2i, 2i + 1) when neighbours is 1
+ * and (i, i + rot_dim / 2) when it is 0, counted from rot_offset.  Pair i turns
+ * by the angle pos[axis_i] * inv_freq[i] radians:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * where pos holds one position per axis for each token (time, height and width
+ * of image and video tokens; one axis for text) and axis_i = axis[i].  The
+ * angle is formed and reduced in fp64, the rotation is fp32, rounded once.
+ *   inv_freq  device fp32 [rot_dim / 2];
+ *   axis      host uint8 [rot_dim / 2], each below n_axes, or NULL (all 0);
+ *             read during the call only.
+ * rot_dim is a multiple of 16 in 16..CSA2_MAX_ROT, rot_offset a multiple of 8,
+ * n_axes 1..3 (CSA2_ERR_INVALID_ARG).
+ */
+enum { CSA2_MAX_ROT = 256, CSA2_MAX_AXES = 3 };
+typedef struct {
+    const float* inv_freq;
+    const uint8_t* axis;
+    int32_t rot_dim;
+    int32_t rot_offset;
+    int32_t neighbours;
+    int32_t n_axes;
+} csa2_rotary;
+
+/*
+ * y = x with its channels rotated, for n_tokens tokens of `heads` heads of
+ * head_dim channels (a multiple of 8, 8..512).  inverse = 1 turns by the
+ * negative angle, which undoes the rotation and is its backward pass (the
+ * gradient of x is the inverse rotation of the gradient of y).  The other
+ * channels are copied.  dtype (x and y): CSA2_DTYPE_BF16, _F16 or _F32.  pos is
+ * device int32 [n_axes][n_tokens].  y may be x itself (same pointer and
+ * strides); otherwise the two must not overlap.  CSA2's latents take their
+ * positions this way before csa2_pack_cache and csa2_sparse_attn.
+ */
+int csa2_rotate(const csa2_rotary* rot, const csa2_heads* x, const csa2_heads* y, int dtype, int64_t n_tokens,
+                int heads, int head_dim, const int32_t* pos, int inverse, csa2_stream stream);
+
+/*
+ * A paged key/value cache of `batch` sequences.  Token t of sequence b, kv head
+ * h, is row t % 64 of page p = page_table[b * max_pages + t / 64]:
+ *   k_pages, v_pages  [num_pages][kv_heads][64][head_dim], dtype CSA2_KV_*;
+ *   n_tokens          device int32 [batch], tokens stored.
+ * head_dim is 64 or 128, kv_heads 1..CSA2_MAX_H, batch 1..CSA2_KV_MAX_BATCH,
+ * max_pages * 64 at most 2^30, num_pages * kv_heads * 64 below 2^31
+ * (CSA2_ERR_UNSUPPORTED beyond).  A CSA2_KV_E4M3 cache holds the nearest E4M3
+ * value (ties to even, saturating at +-448), without a scale, like the FP8
+ * window.  `status` collects CSA2_DEVERR_* bits.  Rows of a page behind
+ * n_tokens may hold anything, NaN included: they never reach a result.
+ */
+#define CSA2_KV_BF16 0
+#define CSA2_KV_F16 1
+#define CSA2_KV_E4M3 2
+#define CSA2_KV_MAX_BATCH 1024
+typedef struct {
+    void* k_pages;
+    void* v_pages;
+    const int32_t* page_table; /* [batch][max_pages] */
+    int32_t* n_tokens;         /* [batch] */
+    uint32_t* status;          /* [1] */
+    int32_t batch;
+    int32_t max_pages;
+    int32_t num_pages;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t dtype;
+} csa2_kv_cache;
+
+/*
+ * New tokens of csa2_kv_append and csa2_kv_attn: `total` rows packed one
+ * sequence after another; sequence b's are rows cu[b] .. cu[b + 1] - 1 (cu:
+ * device int32 [batch + 1], not decreasing, from 0 up to at most total; rows
+ * at and behind cu[batch] are neither read nor written).  A sequence may bring
+ * none.  max_new is a bound that the caller knows: no sequence brings more.  A
+ * sequence whose bounds break these rules sets CSA2_DEVERR_COUNT and is left
+ * out whole.
+ *
+ * csa2_kv_append writes the i-th new token of sequence b to slot start[b] + i
+ * and sets n_tokens[b] = start[b] + (its new tokens).  start is device int32
+ * [batch] apart from n_tokens (a smaller start takes back drafted tokens), or
+ * NULL (or n_tokens itself): append behind the n_tokens held, which costs a
+ * second, small launch.  Keys are rotated by `rot` (NULL: not at all) at pos,
+ * device int32 [n_axes][total]; pos NULL: every axis counts the slots.
+ *   k, v   [total][kv_heads][head_dim], dtype CSA2_DTYPE_BF16 or _F16; the
+ *          cache's dtype is the same type or CSA2_KV_E4M3.
+ * A sequence that does not fit (start[b] < 0 or start[b] + new > max_pages *
+ * 64) sets CSA2_DEVERR_CAPACITY and stays unchanged; a row whose page id lies
+ * outside the pool is skipped with CSA2_DEVERR_PAGE.  Two sequences must not
+ * share the pages that they write.
+ */
+int csa2_kv_append(const csa2_kv_cache* cache, const csa2_heads* k, const csa2_heads* v, int dtype, const int32_t* cu,
+                   int total, int max_new, const int32_t* start, const csa2_rotary* rot, const int32_t* pos,
+                   csa2_stream stream);
+
+/* Workspace bytes csa2_kv_attn needs for these sizes (0: sizes that it refuses). */
+size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new, int H);
+
+/*
+ * Attention of the new tokens over the pages, their own keys (appended before)
+ * included.  The i-th of the m new tokens of a sequence that holds N =
+ * n_tokens[b] stands at position p = N - m + i and sees the keys j <= p, with
+ * window > 0 only those with j > p - window:
+ *   s_j = scale * q[t][h] . k[j][h / (H / kv_heads)],
+ *   out[t][h] = sum_j softmax_j(s) v[j],   lse[t][h] = log(sum_j e^s_j).
+ * A token that sees no key (p < 0) gives zeros and lse = -infinity.
+ *   q, out  [total][H][head_dim], dtype CSA2_DTYPE_BF16 or _F16 (a cache of 16
+ *           bits has the same type); out must not overlap q;
+ *   lse     fp32 [total][H], or NULL.
+ * H is a multiple of kv_heads, at most CSA2_MAX_H; scale is positive.  Sums and softmax statistics
+ * are fp32; the probabilities are rounded to the type of the cache's values
+ * (fp16 for E4M3, whose values, and queries scaled by a power of two per row,
+ * are exact in it within 2^28 of the row's largest magnitude) for the product
+ * with them.  Keys on a page outside the pool are left out with
+ * CSA2_DEVERR_PAGE; n_tokens outside [0, max_pages * 64] is clamped with
+ * CSA2_DEVERR_COUNT.
+ */
+int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dtype, const int32_t* cu, int total,
+                 int max_new, float scale, int window, const csa2_heads* out, float* lse, void* ws, size_t ws_bytes,
+                 csa2_stream stream);
 
 #ifdef __cplusplus
 }
