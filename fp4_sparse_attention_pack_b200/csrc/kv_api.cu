@@ -158,7 +158,7 @@ int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dty
     if (!kv_types_match(dtype, cache->dtype) || total < 0 || max_new < 0 || window < 0 || H < 1 || H > CSA2_MAX_H ||
         H % cache->kv_heads || !std::isfinite(scale) || scale <= 0.0f || !cu)
         return CSA2_ERR_INVALID_ARG;
-    if (total > 1 << 30) return CSA2_ERR_UNSUPPORTED;
+    if ((int64_t)total * H > ((int64_t)1 << 31) - 4096) return CSA2_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     if (total == 0 || max_new == 0) return CSA2_OK;
     if ((rc = check_heads(q, total, H, cache->head_dim, false)) || (rc = check_heads(out, total, H, cache->head_dim, true)))
         return rc;

@@ -1,0 +1,750 @@
+// Attention of a chunk of new tokens over the pages on the 5th-generation tensor
+// cores (tcgen05.mma kind::f16, fp32 accumulation in TMEM).
+//
+// An item is 256 query rows (token, head of the group) of one sequence and kv
+// head: two tiles of 128 rows that share every block of 128 keys.  Per block
+//
+//   S = Q K^T   (M = 128 rows, N = 128 keys, K = head_dim; both from shared memory)
+//   P = 2^(c S - m)   (c = scale log2 e; 16 bits, written over S in TMEM)
+//   O += P V    (M = 128, N = head_dim, K = 128 keys; P from TMEM, V from shared memory)
+//
+// with an online softmax: m is a maximum of an earlier block that moves only when
+// a block exceeds it by more than 8 (then 2^8 fits every type's range), so the
+// rescale of O is rare and the softmax warps do it themselves.  The tensor core
+// works on one tile while the softmax warps work on the other.
+//
+// One CTA per SM, 512 threads, the items' work split evenly (kv_plan.cuh):
+//   warps 0-3, 4-7   softmax of tile 0 and 1: thread = row (TMEM lane); at the
+//                    item's end the output, or the partial sums;
+//   warp 8           issues the MMAs;
+//   warp 9           loads K and V blocks by TMA (16-bit caches): two pages of
+//                    64 rows, 64 channels a box, 128-byte swizzle;
+//   warps 12-15      load the queries of the next item while this one ends; for
+//                    an E4M3 cache they also load K and V and widen them to fp16
+//                    (exact).  Queries are then brought to fp16 as well: a bf16
+//                    row is scaled by a power of two that takes its largest
+//                    magnitude into [2^14, 2^15), undone in c.
+// Rows of V that no row of the item sees (behind the last key, before the
+// window, on a page that is not loaded) are zeroed in shared memory, because
+// 0 x NaN would reach the sums; their scores are masked.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <cstring>
+#include <type_traits>
+
+#include "kv_plan.cuh"
+#include "sm100.cuh"
+
+namespace csa2 {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 256;  // rows of an item
+constexpr int kBlk = 128;   // keys of a block
+constexpr int kOver = 2;    // an item's start and end, in blocks
+constexpr int kThreads = 512;
+constexpr int kWarpMma = 8, kWarpTma = 9, kWarpLoad = 12;
+constexpr int kRing = 16;   // blocks whose masks of bad pages are kept
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // two of each, 128 columns apart
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGap = 8.0f;
+
+enum Mode { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
+constexpr bool is_e4m3(int mode) { return mode >= kE4m3Bf16; }
+
+template <int kDim, int kMode>
+struct __align__(1024) Smem {
+    static constexpr int kSlabs = kDim / 64;
+    static constexpr int kStages = kDim == 64 ? 8 : (is_e4m3(kMode) ? 4 : 5);
+    uint8_t q[2][kSlabs][128 * 128];            // [tile], slabs of 64 channels, SW128
+    uint8_t kv[kStages][kSlabs][kBlk * 128];    // K and V blocks by turns
+    float qc[is_e4m3(kMode) ? 2 : 1][is_e4m3(kMode) ? kTile : 4];  // c of each row (per item parity)
+    uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
+    uint64_t full[kStages], empty[kStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t tail;                              // the TMA of a V block that needs zeroing landed
+    uint64_t drained;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct KvMaps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bounded wait that also gives up when another role has given up.
+template <class S>
+__device__ __forceinline__ bool wait_bar(S& sm, uint64_t* bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (true) {
+        if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+        if (mbar_try_sleep(bar, parity, 20000u)) return true;
+        if (global_ns() - t0 > kWaitNs) {
+            atomicExch(&sm.abort, 1);
+            return false;
+        }
+    }
+}
+template <class S>
+__device__ __forceinline__ bool wait_bar_warp(S& sm, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bar(sm, bar, parity));
+}
+
+template <int n>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf) {
+    uint32_t r;
+    if (bf)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+using Cursor = KvCursor<kTile, kBlk, kOver>;
+
+// Stage counter of the K / V ring.
+template <int kStages>
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++i == kStages) i = 0, phase ^= 1;
+    }
+};
+
+// ---------------------------------------------------------------- MMA
+
+template <int kDim, int kMode>
+__device__ void role_mma(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor cur, uint32_t tb) {
+    using S = Smem<kDim, kMode>;
+    constexpr uint32_t kFmt = kMode == kBf16 ? 1 : 0;
+    const uint32_t idesc_s = idesc_f16(128, kBlk, kFmt, 0, 0);
+    const uint32_t idesc_o = idesc_f16(128, kDim, kFmt, 0, 1);
+    constexpr uint32_t kStageBytes = S::kSlabs * kBlk * 128;
+    const uint64_t desc_q = smem_desc(sm.q[0][0], 16, 1024, kLayoutSw128);
+    const uint64_t desc_k = smem_desc(sm.kv[0][0], 16, 1024, kLayoutSw128);
+    const uint64_t desc_v = smem_desc(sm.kv[0][0], kBlk * 128, 1024, kLayoutSw128);
+    Ring<S::kStages> ring;
+    uint32_t items = 0, np[2] = {0, 0};  // completed items; P hand-overs of each tile
+    KvFrag f;
+    auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
+#pragma unroll
+        for (int ks = 0; ks < kDim / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+            tc_mma_f16_w(tb + kColS + 128 * t, desc_q + off + ((t * S::kSlabs * 128 * 128) >> 4),
+                         desc_k + off + ((stage * kStageBytes) >> 4), idesc_s, ks > 0);
+        }
+        tc_commit_w(&sm.s_full[t]);
+    };
+    while (cur.next(a, g, f)) {
+        const int nb = f.f1 - f.f0, tiles = f.rows > 128 ? 2 : 1;
+        if (nb == 0) continue;
+        if (!wait_bar_warp(sm, &sm.q_full, items & 1)) return;
+        ++items;
+        if (!wait_bar_warp(sm, &sm.full[ring.i], ring.phase)) return;
+        tc_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, ring.i);
+        tc_commit_w(&sm.empty[ring.i]);
+        if (nb == 1) tc_commit_w(&sm.q_empty);
+        ring.step();
+        for (int j = 0; j < nb; ++j) {
+            const int sv = ring.i;
+            const uint32_t pv = ring.phase;
+            ring.step();
+            const int sk = ring.i;
+            const uint32_t pk = ring.phase;
+            const bool more = j + 1 < nb;
+            if (!wait_bar_warp(sm, &sm.full[sv], pv)) return;
+            if (more && !wait_bar_warp(sm, &sm.full[sk], pk)) return;
+            for (int t = 0; t < tiles; ++t) {
+                if (!wait_bar_warp(sm, &sm.p_full[t], np[t] & 1)) return;
+                ++np[t];
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kBlk / 16; ++i)  // O_t += P_t V
+                    tc_mma_f16_ta_w(tb + kColO + 128 * t, tb + kColS + 128 * t + 8 * i,
+                                    desc_v + ((sv * kStageBytes + 2048 * i) >> 4), idesc_o, j > 0 || i > 0);
+                // in order behind the MMAs that read P, which S overwrites
+                if (more) scores(t, sk);
+                else tc_commit_w(&sm.o_done[t]);
+            }
+            tc_commit_w(&sm.empty[sv]);
+            if (more) {
+                tc_commit_w(&sm.empty[sk]);
+                if (j + 2 == nb) tc_commit_w(&sm.q_empty);
+                ring.step();
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- loads
+
+// Pages of a block: ids (or -1: not needed or outside the pool) and bad bits.
+struct PagePair {
+    int p[2];
+    int bad;
+};
+__device__ __forceinline__ PagePair pages_of(const KvAttn& a, const KvFrag& f, int j, int id0, int id1) {
+    PagePair r;
+    r.bad = 0;
+    const int id[2] = {id0, id1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int pg = 2 * j + i;
+        const bool need = pg * PAGE <= f.v.hi && pg * PAGE + PAGE > f.v.lo;
+        const bool good = id[i] >= 0 && id[i] < a.c.num_pages;
+        r.p[i] = need && good ? id[i] : -1;
+        if (need && !good) r.bad |= 1 << i;
+    }
+    return r;
+}
+
+// A row of V that no query row of the item sees, or that is not loaded.
+__device__ __forceinline__ bool v_row_unseen(const KvFrag& f, const PagePair& pp, int j, int r) {
+    const int key = j * kBlk + r;
+    return key < f.v.lo || key > f.v.hi || pp.p[r >> 6] < 0;
+}
+
+template <int kDim, int kMode>
+__device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor cur) {
+    using S = Smem<kDim, kMode>;
+    const int lane = threadIdx.x & 31;
+    Ring<S::kStages> ring;
+    uint32_t used = 0, tails = 0, blocks = 0;
+    KvFrag f;
+    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {  // lanes 0 .. 2 kSlabs - 1, a box each
+        const int i = lane / S::kSlabs, c = lane % S::kSlabs;
+        if (lane < 2 * S::kSlabs && pp.p[i] >= 0)
+            tma_load_2d_nohint(&sm.kv[ring.i][c][i * PAGE * 128], is_v ? &maps.v : &maps.k, 64 * c,
+                               (pp.p[i] * a.c.kv_heads + h) * PAGE, bar);
+        __syncwarp();
+    };
+    bool alive = true;
+    while (alive && cur.next(a, g, f)) {
+        const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
+        int ids = -1;
+        for (int j = f.f0; j < f.f1 && alive; ++j, ++blocks) {
+            if (j == f.f0 || (2 * j & 31) == 0) {  // 32 page ids at a time, one to a lane
+                const int pg = (2 * j & ~31) + lane;
+                ids = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
+            }
+            const PagePair pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids, 2 * j & 31),
+                                         __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31));
+            if (pp.bad && lane == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+            const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * PAGE * kDim * 2;
+            const bool part = j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || pp.bad;
+            for (int is_v = 0; is_v < 2; ++is_v) {
+                if (used >= S::kStages && !(alive = wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1))) break;
+                ++used;
+                uint64_t* full = &sm.full[ring.i];
+                if (!is_v && lane == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
+                __syncwarp();
+                if (!is_v || !part) {
+                    mbar_expect_tx_w(full, bytes);
+                    load(pp, is_v, f.h, full);
+                } else {
+                    if (bytes) {
+                        mbar_expect_tx_w(&sm.tail, bytes);
+                        load(pp, true, f.h, &sm.tail);
+                        // its own copy: waited for even when the others have given up
+                        if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
+                            atomicExch(&sm.abort, 1);
+                            alive = false;
+                            break;
+                        }
+                        ++tails;
+                    }
+                    for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
+                        const int r = (i >> 3) % kBlk;
+                        if (v_row_unseen(f, pp, j, r))
+                            *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    mbar_arrive_w(full);
+                }
+                ring.step();
+            }
+        }
+    }
+    // no copy is in flight when the CTA ends, also after a wait that gave up
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) {
+        for (uint32_t k = 0; k < min(used, (uint32_t)S::kStages); ++k) {
+            const int st = (ring.i + S::kStages - 1 - (int)k) % S::kStages;
+            const uint32_t ph = st < ring.i ? ring.phase : ring.phase ^ 1;
+            (void)mbar_wait(&sm.full[st], ph);
+        }
+    }
+}
+
+// Two channels of E4M3 to fp16 pairs: 16 codes to 32 bytes.
+__device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
+    lo = make_uint4(e4m3x2_to_h2(v.x & 0xFFFF), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y & 0xFFFF), e4m3x2_to_h2(v.y >> 16));
+    hi = make_uint4(e4m3x2_to_h2(v.z & 0xFFFF), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w & 0xFFFF), e4m3x2_to_h2(v.w >> 16));
+}
+
+// Queries (both modes) and, for E4M3, K and V: 128 threads.
+template <int kDim, int kMode>
+__device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor cur) {
+    using S = Smem<kDim, kMode>;
+    const int tid = threadIdx.x - 32 * kWarpLoad;
+    Ring<S::kStages> ring;
+    uint32_t used = 0, items = 0, blocks = 0;
+    const uint32_t inv_g = 65536u / g + 1;  // x / g = x * inv_g >> 16 for x < 256 + g
+    KvFrag f;
+    while (cur.next(a, g, f)) {
+        if (f.f1 == f.f0) continue;
+        // ---- queries
+        if (items > 0 && !wait_bar_warp(sm, &sm.q_empty, (items - 1) & 1)) return;
+        constexpr int kChunks = kDim / 8;  // of 16 bytes a row
+        const int rem0 = f.tile * kTile - f.v.t0 * g;
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) + (int64_t)(f.s.row0 + f.v.t0) * a.q.ts +
+                            (int64_t)f.h * g * a.q.hs;
+        const int rows = f.rows > 128 ? 256 : 128;
+        const int c = tid % kChunks;
+        for (int r0 = tid / kChunks; r0 < rows; r0 += 4 * (128 / kChunks)) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * (128 / kChunks);
+                const int x = rem0 + r, t = (x * inv_g) >> 16;
+                v[k] = make_uint4(0, 0, 0, 0);
+                if (r < f.rows)
+                    v[k] = *reinterpret_cast<const uint4*>(q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * (128 / kChunks);
+                if constexpr (kMode == kE4m3Bf16) {
+                    // largest magnitude's exponent of the row, over the lanes that hold it
+                    uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+                    for (int d = kChunks / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    // the row times 2^e, in two factors that are floats
+                    const int e = top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127);
+                    const int e1 = e / 2, e2 = e - e1;
+                    const float f1 = pow2i(e1), f2 = pow2i(e2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = pack16(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2, false);
+                    v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e * pow2i(-e1) * pow2i(-e2), FLT_MIN);
+                } else if constexpr (kMode == kE4m3F16) {
+                    if (c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e, FLT_MIN);
+                }
+                *reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)]) = v[k];
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_w(&sm.q_full);
+        ++items;
+        if constexpr (is_e4m3(kMode)) {
+            // ---- K and V: a thread's 16 channels of rows r0, r0 + kStep, ...
+            constexpr int kCh = kDim / 16, kStep = 128 / kCh, kN = kBlk / kStep;
+            const int c16 = tid % kCh, r0 = tid / kCh;
+            const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
+            for (int j = f.f0; j < f.f1; ++j, ++blocks) {
+                const int last = f.v.hi / PAGE, first = f.v.lo / PAGE;
+                const PagePair pp = pages_of(a, f, j, 2 * j >= first && 2 * j <= last ? table[2 * j] : -1,
+                                             2 * j + 1 >= first && 2 * j + 1 <= last ? table[2 * j + 1] : -1);
+                if (pp.bad && tid == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+                uint4 v[2][kN];
+#pragma unroll
+                for (int is_v = 0; is_v < 2; ++is_v)
+#pragma unroll
+                    for (int k = 0; k < kN; ++k) {
+                        const int r = r0 + k * kStep, p = r < 64 ? pp.p[0] : pp.p[1];
+                        v[is_v][k] = make_uint4(0, 0, 0, 0);
+                        if (p >= 0 && !(is_v && v_row_unseen(f, pp, j, r)))
+                            v[is_v][k] = *reinterpret_cast<const uint4*>(
+                                (is_v ? a.c.v : a.c.k) + (((int64_t)p * a.c.kv_heads + f.h) * PAGE + (r & 63)) * kDim + 16 * c16);
+                    }
+#pragma unroll
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
+                    ++used;
+                    if (!is_v && tid == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
+#pragma unroll
+                    for (int k = 0; k < kN; ++k) {
+                        const int r = r0 + k * kStep;
+                        uint4 lo, hi;
+                        widen16(v[is_v][k], lo, hi);
+                        uint8_t* slab = sm.kv[ring.i][c16 >> 2];
+                        const int ch = 2 * (c16 & 3);
+                        *reinterpret_cast<uint4*>(slab + sw128(r, ch)) = lo;
+                        *reinterpret_cast<uint4*>(slab + sw128(r, ch + 1)) = hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    mbar_arrive_w(&sm.full[ring.i]);
+                    ring.step();
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+
+template <int kDim, int kMode>
+__device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, Cursor cur,
+                             uint32_t tb) {
+    const int t = threadIdx.x >> 7, row = threadIdx.x & 127;  // tile; row = TMEM lane
+    const uint32_t lane_base = tb + ((uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16);
+    const uint32_t ts = lane_base + kColS + 128 * t, to = lane_base + kColO + 128 * t;
+    constexpr bool kP16Bf = kMode == kBf16;  // P in V's type
+    constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
+    uint32_t ns = 0, no = 0, items = 0, blocks = 0;
+    KvFrag f;
+    while (cur.next(a, g, f)) {
+        const int nb = f.f1 - f.f0;
+        const int it = items;
+        if (nb > 0) ++items;
+        const int blk0 = blocks;
+        blocks += nb;
+        if (f.rows <= 128 * t) continue;
+        const int x = min(f.tile * kTile - f.v.t0 * g + 128 * t + row, f.tile * kTile - f.v.t0 * g + f.rows - 1);
+        const int tok = f.v.t0 + x / g, hd = x % g;
+        const int pos = f.s.n - f.s.m + tok;                        // the row sees keys lo .. pos
+        const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        float mref = -INFINITY, l = 0.0f;
+        float c = fmaxf(a.scale * kLog2e, FLT_MIN);  // never 0: a masked score is -infinity
+        for (int j = f.f0; j < f.f1; ++j) {
+            if (!wait_bar_warp(sm, &sm.s_full[t], ns & 1)) return;
+            ++ns;
+            __syncwarp();
+            tc_fence_after();
+            if constexpr (is_e4m3(kMode)) {
+                if (j == f.f0) c = sm.qc[it & 1][128 * t + row];
+            }
+            float s[128];
+            {
+                uint32_t r0[32], r1[32], r2[32], r3[32];
+                tmem_ld_x32_nowait(ts, r0);
+                tmem_ld_x32_nowait(ts + 32, r1);
+                tmem_ld_x32_nowait(ts + 64, r2);
+                tmem_ld_x32_nowait(ts + 96, r3);
+                tmem_wait_ld2(r0, r1);
+                tmem_wait_ld2(r2, r3);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    s[i] = __uint_as_float(r0[i]);
+                    s[32 + i] = __uint_as_float(r1[i]);
+                    s[64 + i] = __uint_as_float(r2[i]);
+                    s[96 + i] = __uint_as_float(r3[i]);
+                }
+            }
+            const int bad = sm.bad[(blk0 + j - f.f0) % kRing];
+            const int c_hi = pos - j * kBlk, c_lo = lo - j * kBlk;
+            if (__any_sync(0xffffffffu, c_hi < kBlk - 1 || c_lo > 0) || bad) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i > c_hi || i < c_lo || (bad & (i < 64 ? 1 : 2))) s[i] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = i + 4 + k < 128 ? fmaxf(fmaxf(mx[k], s[i + k]), s[i + 4 + k]) : fmaxf(mx[k], s[i + k]);
+            }
+            const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool move = bm > mref + kGap || (mref == -INFINITY && bm > -INFINITY);
+            if (__any_sync(0xffffffffu, move)) {
+                const float f1 = move ? ex2(mref - bm) : 1.0f;  // mref = -inf: 0
+                if (move) mref = bm;
+                l *= f1;
+                if (j > f.f0) {  // O holds the blocks before
+#pragma unroll 1
+                    for (int k = 0; k < kDim; k += 16) {
+                        float o[16];
+                        tmem_ld_32x32b_x16(to + k, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= f1;
+                        tmem_st_32x32b_x16(to + k, o);
+                    }
+                }
+            }
+            const float ms = mref == -INFINITY ? 0.0f : mref;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float p[64];  // two 16-bit values each
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const float e0 = ex2(fmaf(s[2 * i], c, -ms)), e1 = ex2(fmaf(s[2 * i + 1], c, -ms));
+                sum[(2 * i) & 3] += e0;
+                sum[(2 * i + 1) & 3] += e1;
+                p[i] = __uint_as_float(pack16(e0, e1, kP16Bf));
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_32x32b_x64(ts, p);
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_w(&sm.p_full[t]);
+        }
+        // ---- the item's end
+        if (nb > 0) {
+            if (!wait_bar_warp(sm, &sm.o_done[t], no & 1)) return;
+            ++no;
+            __syncwarp();
+            tc_fence_after();
+        }
+        const bool mine = 128 * t + row < f.rows;
+        if (f.first && f.last) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int64_t token = f.s.row0 + tok;
+            const int head = f.h * g + hd;
+            uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
+#pragma unroll 1
+            for (int k = 0; k < kDim; k += 32) {
+                float o[32];
+                if (nb > 0) tmem_ld_32x32b_x32(to + k, o);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv, kOutBf);
+                    if (mine) *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (mine && a.lse) a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
+        } else {
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
+            float4* po = parts.o + slot * (kDim / 4) * kTile + 128 * t + row;
+#pragma unroll 1
+            for (int k = 0; k < kDim; k += 32) {
+                float o[32];
+                tmem_ld_32x32b_x32(to + k, o);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+            parts.ml[slot * kTile + 128 * t + row] = make_float2(mref, l);
+            if (f.first && threadIdx.x == 0)
+                parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+        }
+        tc_fence_before();
+        __syncwarp();
+    }
+}
+
+template <int kDim, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv_mma(const __grid_constant__ KvAttn a, const __grid_constant__ KvMaps maps, const __grid_constant__ KvPlan plan,
+             const __grid_constant__ KvParts parts) {
+    extern __shared__ uint8_t smem_raw[];
+    using S = Smem<kDim, kMode>;
+    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    static_assert(sizeof(KvPlanSmem) <= sizeof(sm.kv), "the plan's arrays lie in the ring");
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sm.full[i], is_e4m3(kMode) ? 4 : 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.q_full, 4);
+        mbar_init(&sm.q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.o_done[t], 1);
+        }
+        mbar_init(&sm.tail, 1);
+        mbar_init(&sm.drained, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+        parts.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
+    }
+    if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, kTmemCols);
+    int64_t per;
+    Cursor cur = kv_plan<kTile, kBlk, kOver>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
+    // 128 registers a thread at launch; the softmax warps take what the others give up
+    if (warp < 8) {
+        regs_up<176>();
+        role_softmax<kDim, kMode>(sm, a, parts, per, plan.g, cur, tb);
+    } else {
+        regs_down<80>();
+        if (warp == kWarpMma) role_mma<kDim, kMode>(sm, a, plan.g, cur, tb);
+        else if (warp == kWarpTma && !is_e4m3(kMode)) role_tma<kDim, kMode>(sm, a, maps, plan.g, cur);
+        else if (warp >= kWarpLoad) role_load<kDim, kMode>(sm, a, plan.g, cur);
+    }
+    __syncwarp();
+    __syncthreads();
+    if (sm.abort && tid == 0) atomicOr(a.c.status, CSA2_DEVERR_TIMEOUT);
+    if (warp == kWarpMma) {  // every MMA has completed before TMEM is freed
+        tc_commit_w(&sm.drained);
+        (void)mbar_wait_warp(&sm.drained, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tb, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- join
+
+// The items that a range's end divides: blockIdx.x the CTA that begins it,
+// blockIdx.y 32 of its rows (a warp's lanes); the warps share the channels.
+template <int kDim, bool kBf>
+__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttn a, const __grid_constant__ KvParts parts,
+                                                 int g, int tile_rows) {
+    cudaGridDependencySynchronize();
+    const int cta = blockIdx.x;
+    const int4 cut = parts.cut[cta];
+    if (cut.w < 0) return;
+    const KvSeq s = kv_seq(a, cut.x);
+    const int row = 32 * blockIdx.y + (threadIdx.x & 31);
+    const int64_t r = (int64_t)cut.z * tile_rows + row;
+    if (r >= (int64_t)s.m * g) return;
+    float M = -INFINITY, L = 0.0f;
+    for (int k = cta; k <= cut.w; ++k) {
+        const float2 ml = parts.ml[(2 * (int64_t)k + (k == cta)) * tile_rows + row];
+        M = fmaxf(M, ml.x);
+    }
+    const float Ms = M == -INFINITY ? 0.0f : M;
+    float4 acc[kDim / 16];
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = cta; k <= cut.w; ++k) {
+        const int64_t slot = 2 * (int64_t)k + (k == cta);
+        const float2 ml = parts.ml[slot * tile_rows + row];
+        const float w = exp2f(ml.x - Ms);
+        L += ml.y * w;
+#pragma unroll
+        for (int i = 0; i < kDim / 16; ++i) {
+            const float4 o = parts.o[(slot * (kDim / 4) + (threadIdx.x >> 5) + 4 * i) * tile_rows + row];
+            acc[i].x += w * o.x, acc[i].y += w * o.y, acc[i].z += w * o.z, acc[i].w += w * o.w;
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int64_t token = s.row0 + r / g;
+    const int head = cut.y * g + (int)(r % g);
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) {
+        uint2 w = make_uint2(pack16(acc[i].x * inv, acc[i].y * inv, kBf), pack16(acc[i].z * inv, acc[i].w * inv, kBf));
+        if (L == 0.0f) w = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(out + 4 * ((threadIdx.x >> 5) + 4 * i)) = w;
+    }
+    if (a.lse && threadIdx.x < 32) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 kv_encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    }();
+    return fn;
+}
+
+// A pool as rows of head_dim 16-bit channels; boxes of 64 channels x 64 rows.
+bool make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int dim, bool bf) {
+    auto fn = kv_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)dim * 2};
+    cuuint32_t box[2] = {64, PAGE};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch `kernel` so that its start overlaps the end of the launch before it.
+template <typename... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kDim, int kMode>
+cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
+    using S = Smem<kDim, kMode>;
+    constexpr int kSmem = sizeof(S) + 1024;
+    static_assert(kSmem <= 232448, "shared memory beyond the 227 KB per-block limit");
+    KvMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!is_e4m3(kMode)) {
+        const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
+        if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode == kBf16) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode == kBf16))
+            return cudaErrorInvalidValue;
+    }
+    KvPlan plan;
+    plan.g = a.H / a.c.kv_heads;
+    plan.grid = device_sm_count();
+    plan.min_per = 4;
+    const KvParts parts = kv_parts(a.ws, plan.grid, kTile, kDim);
+    static std::atomic<uint64_t> attr_done{0};
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_mma<kDim, kMode>), kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    k_kv_mma<kDim, kMode><<<plan.grid, kThreads, kSmem, st>>>(a, maps, plan, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    constexpr bool kBf = kMode == kBf16 || kMode == kE4m3Bf16;
+    return launch_behind(k_kv_join<kDim, kBf>, dim3(plan.grid, kTile / 32), 128, st, a, parts, plan.g, kTile);
+}
+
+}  // namespace
+
+size_t kv_mma_workspace_bytes(int head_dim) { return kv_parts_bytes(device_sm_count(), kTile, head_dim); }
+
+cudaError_t launch_kv_mma(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st) {
+    const bool e4m3 = kv_dtype == CSA2_KV_E4M3, bf = dtype == CSA2_DTYPE_BF16;
+    if (head_dim == 64)
+        return e4m3 ? (bf ? mma_as<64, kE4m3Bf16>(a, st) : mma_as<64, kE4m3F16>(a, st))
+                    : (bf ? mma_as<64, kBf16>(a, st) : mma_as<64, kF16>(a, st));
+    return e4m3 ? (bf ? mma_as<128, kE4m3Bf16>(a, st) : mma_as<128, kE4m3F16>(a, st))
+                : (bf ? mma_as<128, kBf16>(a, st) : mma_as<128, kF16>(a, st));
+}
+
+}  // namespace csa2

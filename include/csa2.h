@@ -616,7 +616,8 @@ size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new
  *   q, out  [total][H][head_dim], dtype CSA2_DTYPE_BF16 or _F16 (a cache of 16
  *           bits has the same type); out must not overlap q;
  *   lse     fp32 [total][H], or NULL.
- * H is a multiple of kv_heads, at most CSA2_MAX_H; scale is positive.  Sums and softmax statistics
+ * H is a multiple of kv_heads, at most CSA2_MAX_H; total * H is below 2^31 - 4096;
+ * scale is positive.  Sums and softmax statistics
  * are fp32; the probabilities are rounded to the type of the cache's values
  * (fp16 for E4M3, whose values, and queries scaled by a power of two per row,
  * are exact in it within 2^28 of the row's largest magnitude) for the product

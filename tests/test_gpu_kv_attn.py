@@ -225,7 +225,11 @@ def test_two_streams_at_once(csa):
     for c in cs:
         c.hold_all()
     torch.cuda.synchronize()
-    got = [[c.attend(0.1, stream=s) for _ in range(3)] for c, s in zip(cs, streams)]
+    got = [[], []]
+    for _ in range(3):
+        for c, s, outs in zip(cs, streams, got):
+            with torch.cuda.stream(s):  # the outputs and the workspace are filled on it as well
+                outs.append(c.attend(0.1))
     torch.cuda.synchronize()
     for c, outs in zip(cs, got):
         for o, l in outs:
