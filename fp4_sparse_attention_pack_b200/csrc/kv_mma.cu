@@ -36,6 +36,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "kv_attn.cuh"
 #include "kv_plan.cuh"
 #include "sm100.cuh"
 
@@ -53,13 +54,6 @@ constexpr int kWarpMma = 8, kWarpTma = 9, kWarpLoad = 12;
 constexpr int kRing = 16;   // blocks whose masks of bad pages are kept
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // two of each, 128 columns apart
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGap = 8.0f;
-
-enum Mode { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
-constexpr bool is_e4m3(int mode) { return mode >= kE4m3Bf16; }
-
 template <int kDim, int kMode>
 struct __align__(1024) Smem {
     static constexpr int kSlabs = kDim / 64;
@@ -77,17 +71,7 @@ struct __align__(1024) Smem {
     int abort;
 };
 
-struct KvMaps {
-    CUtensorMap k, v;
-};
-
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Bounded wait that also gives up when another role has given up.
 template <class S>
@@ -115,15 +99,6 @@ __device__ __forceinline__ void regs_up() {
 template <int n>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
-}
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf) {
-    uint32_t r;
-    if (bf)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 using Cursor = KvCursor<kTile, kBlk, kOver>;
@@ -344,22 +319,8 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
             for (int k = 0; k < 4; ++k) {
                 const int r = r0 + k * (128 / kChunks);
                 if constexpr (kMode == kE4m3Bf16) {
-                    // largest magnitude's exponent of the row, over the lanes that hold it
-                    uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-#pragma unroll
-                    for (int d = kChunks / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    // the row times 2^e, in two factors that are floats
-                    const int e = top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127);
-                    const int e1 = e / 2, e2 = e - e1;
-                    const float f1 = pow2i(e1), f2 = pow2i(e2);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = pack16(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2, false);
-                    v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e * pow2i(-e1) * pow2i(-e2), FLT_MIN);
+                    const float k2 = scale_row<kChunks>(v[k], fmaxf(a.scale * kLog2e, FLT_MIN));
+                    if (c == 0) sm.qc[items & 1][r] = k2;
                 } else if constexpr (kMode == kE4m3F16) {
                     if (c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e, FLT_MIN);
                 }
@@ -619,94 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// ---------------------------------------------------------------- join
-
-// The items that a range's end divides: blockIdx.x the CTA that begins it,
-// blockIdx.y 32 of its rows (a warp's lanes); the warps share the channels.
-template <int kDim, bool kBf>
-__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttn a, const __grid_constant__ KvParts parts,
-                                                 int g, int tile_rows) {
-    cudaGridDependencySynchronize();
-    const int cta = blockIdx.x;
-    const int4 cut = parts.cut[cta];
-    if (cut.w < 0) return;
-    const KvSeq s = kv_seq(a, cut.x);
-    const int row = 32 * blockIdx.y + (threadIdx.x & 31);
-    const int64_t r = (int64_t)cut.z * tile_rows + row;
-    if (r >= (int64_t)s.m * g) return;
-    float M = -INFINITY, L = 0.0f;
-    for (int k = cta; k <= cut.w; ++k) {
-        const float2 ml = parts.ml[(2 * (int64_t)k + (k == cta)) * tile_rows + row];
-        M = fmaxf(M, ml.x);
-    }
-    const float Ms = M == -INFINITY ? 0.0f : M;
-    float4 acc[kDim / 16];
-#pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = cta; k <= cut.w; ++k) {
-        const int64_t slot = 2 * (int64_t)k + (k == cta);
-        const float2 ml = parts.ml[slot * tile_rows + row];
-        const float w = exp2f(ml.x - Ms);
-        L += ml.y * w;
-#pragma unroll
-        for (int i = 0; i < kDim / 16; ++i) {
-            const float4 o = parts.o[(slot * (kDim / 4) + (threadIdx.x >> 5) + 4 * i) * tile_rows + row];
-            acc[i].x += w * o.x, acc[i].y += w * o.y, acc[i].z += w * o.z, acc[i].w += w * o.w;
-        }
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const int64_t token = s.row0 + r / g;
-    const int head = cut.y * g + (int)(r % g);
-    uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
-#pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) {
-        uint2 w = make_uint2(pack16(acc[i].x * inv, acc[i].y * inv, kBf), pack16(acc[i].z * inv, acc[i].w * inv, kBf));
-        if (L == 0.0f) w = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(out + 4 * ((threadIdx.x >> 5) + 4 * i)) = w;
-    }
-    if (a.lse && threadIdx.x < 32) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 kv_encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-    }();
-    return fn;
-}
-
-// A pool as rows of head_dim 16-bit channels; boxes of 64 channels x 64 rows.
-bool make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int dim, bool bf) {
-    auto fn = kv_encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)dim * 2};
-    cuuint32_t box[2] = {64, PAGE};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
-              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Launch `kernel` so that its start overlaps the end of the launch before it.
-template <typename... Args>
-cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int kDim, int kMode>
 cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     using S = Smem<kDim, kMode>;
@@ -716,7 +589,7 @@ cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     std::memset(&maps, 0, sizeof(maps));
     if (!is_e4m3(kMode)) {
         const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
-        if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode == kBf16) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode == kBf16))
+        if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode))
             return cudaErrorInvalidValue;
     }
     KvPlan plan;

@@ -1,0 +1,547 @@
+// Attention over the pages for few query rows (a decode step, drafted tokens): at
+// most 16 or 32 rows (token, head of the group) to a sequence and kv head.
+//
+// Every key and value is read once and used for all the rows, some 2 x rows
+// flops a byte, so the cache's bytes bound it.  A page of 64 keys is a stage of
+// a TMA ring (about 96 KB in flight in each of two CTAs an SM); warp w of four
+// takes its keys 16 w .. 16 w + 15 with an online softmax of its own, so the
+// warps meet only at an item's end:
+//
+//   S = Q K^T   mma m16n8k16 (rows x 16 keys, K = head_dim)
+//   P = 2^(c S - m), kept in registers: the accumulators of S are P's operand
+//   O += P V    mma m16n8k16 (K = 16 keys)
+//
+// (mma.sync, not tcgen05: 16 or 32 rows of its 128 would be used, and the
+// operands come out of registers without a hand-over.)  An E4M3 cache is widened
+// to fp16 in registers (exact): two bytes of a key's fragment are neighbouring
+// channels, so Q is read with its channels in the same order; two bytes of a
+// value's (transposed) fragment are two channels of one key, which byte
+// permutations pair by key.  Queries are scaled per row as in kv_mma.cu.
+// The work is cut evenly over the CTAs (kv_plan.cuh), which splits long
+// sequences when there are few.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <cstring>
+
+#include "kv_attn.cuh"
+#include "kv_plan.cuh"
+#include "sm100.cuh"
+
+namespace csa2 {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kOver = 3;       // an item's start and end, in pages
+constexpr int kMinPer = 6;     // least cost of a CTA's range
+constexpr int kCtasPerSm = 2;
+
+template <int kDim, int kMode, int kMT>
+struct __align__(1024) Smem {
+    static constexpr int kElem = is_e4m3(kMode) ? 1 : 2;
+    static constexpr int kRowBytes = kDim * kElem < 128 ? kDim * kElem : 128;  // of a slab
+    static constexpr int kSlabs = kDim * kElem / kRowBytes;
+    static constexpr int kPageBytes = PAGE * kDim * kElem;
+    static constexpr int kQStride = kDim * 2 + 16;
+    static constexpr int kRedBytes = 2 * 16 * kMT * kDim * 4;  // two warps' sums
+    static constexpr int kRoom = 112 * 1024 - kRedBytes - 16 * kMT * kQStride - 2048;
+    static constexpr int kStages = kRoom / (2 * kPageBytes) < 12 ? kRoom / (2 * kPageBytes) : 12;
+    uint8_t kv[kStages][2][kPageBytes];
+    uint8_t q[16 * kMT][kQStride];
+    float red[2][16 * kMT][kDim];
+    float ml[kWarps][16 * kMT][2];
+    float qc[16 * kMT];
+    uint8_t bad[kStages];
+    uint64_t full[kStages], empty[kStages];
+    int abort;
+};
+
+template <class S>
+__device__ __forceinline__ bool wait_bar_warp(S& sm, uint64_t* bar, uint32_t parity) {
+    bool ok = mbar_try(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t t0 = global_ns();
+        while (!ok) {
+            if (*reinterpret_cast<volatile int*>(&sm.abort)) break;
+            ok = mbar_try_sleep(bar, parity, 20000u);
+            if (!ok && global_ns() - t0 > kWaitNs) {
+                atomicExch(&sm.abort, 1);
+                break;
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+}
+
+// Byte offset of 16-byte chunk c (of the whole row) of a page's row r: slabs of
+// 128-byte rows with the 128-byte swizzle, or 64-byte rows with the 64-byte one.
+template <class S>
+__device__ __forceinline__ uint32_t at16(int r, int c) {
+    if constexpr (S::kRowBytes == 128) return (c >> 3) * (PAGE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <bool kBf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kBf)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+template <int kMT>
+using Cursor = KvCursor<16 * kMT, PAGE, kOver>;
+
+// ---------------------------------------------------------------- loads
+
+template <int kDim, int kMode, int kMT>
+__device__ void role_load(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor<kMT> cur) {
+    using S = Smem<kDim, kMode, kMT>;
+    const int lane = threadIdx.x & 31;
+    int st = 0;
+    uint32_t phase = 0, used = 0;
+    KvFrag f;
+    bool alive = true;
+    while (alive && cur.next(a, g, f)) {
+        const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
+        int ids = -1;
+        for (int j = f.f0; j < f.f1; ++j) {
+            if (j == f.f0 || (j & 31) == 0) {  // 32 page ids at a time, one to a lane
+                const int pg = (j & ~31) + lane;
+                ids = pg >= f.f0 && pg < f.f1 ? table[pg] : -1;
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+            const bool good = id >= 0 && id < a.c.num_pages;
+            if (used >= S::kStages && !(alive = wait_bar_warp(sm, &sm.empty[st], phase ^ 1))) break;
+            ++used;
+            if (lane == 0) {
+                sm.bad[st] = !good;
+                if (!good) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+            }
+            __syncwarp();
+            mbar_expect_tx_w(&sm.full[st], good ? 2 * S::kPageBytes : 0);
+            if (good && lane < 2 * S::kSlabs) {
+                const int v = lane / S::kSlabs, c = lane % S::kSlabs;
+                tma_load_2d_nohint(&sm.kv[st][v][c * PAGE * S::kRowBytes], v ? &maps.v : &maps.k,
+                                   c * (S::kRowBytes / S::kElem), (id * a.c.kv_heads + f.h) * PAGE, &sm.full[st]);
+            }
+            __syncwarp();
+            if (++st == S::kStages) st = 0, phase ^= 1;
+        }
+    }
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) {  // no copy is in flight when the CTA ends
+        for (uint32_t k = 0; k < min(used, (uint32_t)S::kStages); ++k) {
+            const int s = (st + S::kStages - 1 - (int)k) % S::kStages;
+            (void)mbar_wait(&sm.full[s], s < st ? phase : phase ^ 1);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- rows
+
+template <int kDim, int kMode, int kMT>
+__device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g,
+                          Cursor<kMT> cur) {
+    using S = Smem<kDim, kMode, kMT>;
+    constexpr bool kBf = kMode == kBf16;                           // operands
+    constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;  // q and out
+    constexpr int kRows = 16 * kMT, kKs = kDim / 16, kNt = kDim / 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
+    const float c0 = fmaxf(a.scale * kLog2e, FLT_MIN);
+    int st = 0;
+    uint32_t phase = 0;
+    KvFrag f;
+    while (cur.next(a, g, f)) {
+        const int nb = f.f1 - f.f0;
+        if (nb > 0) {
+            // ---- the item's queries, in the operands' type
+            constexpr int kCh = kDim / 8;  // 16-byte chunks of a row
+            for (int i = threadIdx.x; i < kRows * kCh; i += 32 * kWarps) {
+                const int r = i / kCh, c = i % kCh;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < f.rows) {
+                    const int t = r / g;
+                    v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q.p) +
+                                                        (int64_t)(f.s.row0 + t) * a.q.ts +
+                                                        (int64_t)(f.h * g + r - t * g) * a.q.hs + 8 * c);
+                }
+                if constexpr (kMode == kE4m3Bf16) {
+                    const float k = scale_row<kCh>(v, c0);
+                    if (c == 0) sm.qc[r] = k;
+                }
+                *reinterpret_cast<uint4*>(&sm.q[r][16 * c]) = v;
+            }
+            warps_sync();
+        }
+        uint32_t qf[kMT == 1 ? kKs : 1][4];
+        auto load_q = [&](int mt, int ks, uint32_t (&r)[4]) {
+            if constexpr (is_e4m3(kMode)) {  // channels 4 c .. 4 c + 3 of the 16
+                const uint2 x = *reinterpret_cast<const uint2*>(&sm.q[16 * mt + quad][32 * ks + 8 * qc]);
+                const uint2 y = *reinterpret_cast<const uint2*>(&sm.q[16 * mt + quad + 8][32 * ks + 8 * qc]);
+                r[0] = x.x, r[1] = y.x, r[2] = x.y, r[3] = y.y;
+            } else {
+                ldsm4(smem_u32(&sm.q[16 * mt + (lane & 15)][32 * ks + 16 * (lane >> 4)]), r);
+            }
+        };
+        int pos[kMT][2], lo[kMT][2];
+        float cc[kMT][2], mref[kMT][2], l[kMT][2];
+        float o[kMT][kNt][4];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = min(16 * mt + quad + 8 * e, f.rows - 1);
+                pos[mt][e] = f.s.n - f.s.m + r / g;
+                lo[mt][e] = a.window > 0 ? max(0, pos[mt][e] - a.window + 1) : 0;
+                cc[mt][e] = kMode == kE4m3Bf16 && nb > 0 ? sm.qc[16 * mt + quad + 8 * e] : c0;
+                mref[mt][e] = -INFINITY, l[mt][e] = 0.0f;
+            }
+        const int pos_min = f.s.n - f.s.m, lo_max = a.window > 0 ? max(0, f.v.hi - a.window + 1) : 0;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int t = 0; t < kNt; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.0f;
+        if constexpr (kMT == 1) {
+            if (nb > 0) {
+#pragma unroll
+                for (int ks = 0; ks < kKs; ++ks) load_q(0, ks, qf[ks]);
+            }
+        }
+        for (int j = f.f0; j < f.f1; ++j) {
+            if (!wait_bar_warp(sm, &sm.full[st], phase)) return;
+            const int kb = j * PAGE + 16 * warp;  // the warp's keys
+            if (!sm.bad[st] && kb <= f.v.hi && kb + 15 >= f.v.lo) {
+                const uint32_t kp = smem_u32(sm.kv[st][0]), vp = smem_u32(sm.kv[st][1]);
+                const bool edge = kb + 15 > f.v.hi || kb < f.v.lo;
+                if (edge) {  // rows of V that no query sees: zero, as 0 x NaN is not
+                    for (int i = lane; i < 16 * (kDim * S::kElem / 16); i += 32) {
+                        const int r = i & 15, key = kb + r;
+                        if (key > f.v.hi || key < f.v.lo)
+                            *reinterpret_cast<uint4*>(sm.kv[st][1] + at16<S>(16 * warp + r, i >> 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();  // the stage is next written by a TMA
+                    __syncwarp();
+                }
+                // ---- S
+                float s[kMT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.0f;
+                const int kr = 16 * warp + (lane & 7) + ((lane >> 4) << 3);  // ldmatrix row of this lane
+                if constexpr (!is_e4m3(kMode)) {
+#pragma unroll
+                    for (int ks = 0; ks < kKs; ++ks) {
+                        uint32_t b[4];
+                        ldsm4(kp + at16<S>(kr, 2 * ks + ((lane >> 3) & 1)), b);
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            uint32_t q2[4];
+                            if constexpr (kMT > 1) load_q(mt, ks, q2);
+                            const uint32_t(&q)[4] = kMT == 1 ? qf[kMT == 1 ? ks : 0] : q2;
+                            mma16816<kBf>(s[mt][0], q, b[0], b[1]);
+                            mma16816<kBf>(s[mt][1], q, b[2], b[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < kKs; ks += 2) {
+                        uint32_t b[4];  // (keys 0-7, 16 channels), (keys 0-7, next 16), (keys 8-15, ..)
+                        ldsm4(kp + at16<S>(kr, ks + ((lane >> 3) & 1)), b);
+#pragma unroll
+                        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                            for (int mt = 0; mt < kMT; ++mt) {
+                                uint32_t q2[4];
+                                if constexpr (kMT > 1) load_q(mt, ks + k2, q2);
+                                const uint32_t(&q)[4] = kMT == 1 ? qf[kMT == 1 ? ks + k2 : 0] : q2;
+                                mma16816<false>(s[mt][0], q, e4m3x2_to_h2(b[k2] & 0xFFFF), e4m3x2_to_h2(b[k2] >> 16));
+                                mma16816<false>(s[mt][1], q, e4m3x2_to_h2(b[2 + k2] & 0xFFFF), e4m3x2_to_h2(b[2 + k2] >> 16));
+                            }
+                    }
+                }
+                // ---- softmax: elements 0, 1 of row quad, 2, 3 of row quad + 8
+                if (kb + 15 > pos_min || kb < lo_max) {
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = kb + 8 * t + 2 * qc + (e & 1);
+                                if (key > pos[mt][e >> 1] || key < lo[mt][e >> 1]) s[mt][t][e] = -INFINITY;
+                            }
+                }
+                float bm[kMT][2];
+                bool move = false;
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]), fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        bm[mt][e] = x * cc[mt][e];
+                        move = move || bm[mt][e] > mref[mt][e] + kGap || (mref[mt][e] == -INFINITY && bm[mt][e] > -INFINITY);
+                    }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mn = fmaxf(mref[mt][e], bm[mt][e]);
+                            const float x = mn == -INFINITY ? 1.0f : ex2(mref[mt][e] - mn);
+                            mref[mt][e] = mn;
+                            l[mt][e] *= x;
+#pragma unroll
+                            for (int t = 0; t < kNt; ++t) o[mt][t][2 * e] *= x, o[mt][t][2 * e + 1] *= x;
+                        }
+                }
+                uint32_t p[kMT][4];
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float ms = mref[mt][e] == -INFINITY ? 0.0f : mref[mt][e];
+                            const float x = ex2(fmaf(s[mt][t][2 * e], cc[mt][e], -ms));
+                            const float y = ex2(fmaf(s[mt][t][2 * e + 1], cc[mt][e], -ms));
+                            l[mt][e] += x + y;
+                            p[mt][2 * t + e] = pack16(x, y, kBf);
+                        }
+                // ---- O
+                const int vr = 16 * warp + (lane & 15);
+                if constexpr (!is_e4m3(kMode)) {
+#pragma unroll
+                    for (int t = 0; t < kNt; t += 2) {
+                        uint32_t b[4];  // (keys 0-7, 8 channels), (keys 8-15, ..), the next 8 channels
+                        ldsm4t(vp + at16<S>(vr, t + (lane >> 4)), b);
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            mma16816<kBf>(o[mt][t], p[mt], b[0], b[1]);
+                            mma16816<kBf>(o[mt][t + 1], p[mt], b[2], b[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < kNt; t += 4) {
+                        uint32_t b[4];  // (keys 0-7, 16 channels), (keys 8-15, ..), the next 16 channels
+                        ldsm4t(vp + at16<S>(vr, t / 2 + (lane >> 4)), b);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            // even channels: bytes 0, 2 (keys 2 c, 2 c + 1); odd ones: bytes 1, 3
+                            const uint32_t e0 = e4m3x2_to_h2(__byte_perm(b[2 * u], 0, 0x4420)), e1 = e4m3x2_to_h2(__byte_perm(b[2 * u + 1], 0, 0x4420));
+                            const uint32_t d0 = e4m3x2_to_h2(__byte_perm(b[2 * u], 0, 0x4431)), d1 = e4m3x2_to_h2(__byte_perm(b[2 * u + 1], 0, 0x4431));
+#pragma unroll
+                            for (int mt = 0; mt < kMT; ++mt) {
+                                mma16816<false>(o[mt][t + 2 * u], p[mt], e0, e1);
+                                mma16816<false>(o[mt][t + 2 * u + 1], p[mt], d0, d1);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            mbar_arrive_w(&sm.empty[st]);
+            if (++st == S::kStages) st = 0, phase ^= 1;
+        }
+        // ---- the warps' sums over their keys, joined in a fixed order
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
+                l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
+                if (qc == 0) {
+                    sm.ml[warp][16 * mt + quad + 8 * e][0] = mref[mt][e];
+                    sm.ml[warp][16 * mt + quad + 8 * e][1] = l[mt][e];
+                }
+            }
+        warps_sync();
+        float w[kMT][2];  // weight of this warp's sums
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * mt + quad + 8 * e;
+                const float M = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
+                w[mt][e] = M == -INFINITY ? 0.0f : ex2(mref[mt][e] - M);
+            }
+        // channel of element e of accumulator t: neighbouring pairs, but for E4M3 every other one
+        auto place = [&](bool add, int buf) {
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int t = 0; t < kNt; t += is_e4m3(kMode) ? 2 : 1)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float* row = sm.red[buf][16 * mt + quad + 8 * e];
+                        if constexpr (is_e4m3(kMode)) {
+                            float4* d = reinterpret_cast<float4*>(row + 8 * t + 4 * qc);
+                            float4 v = make_float4(o[mt][t][2 * e], o[mt][t + 1][2 * e], o[mt][t][2 * e + 1], o[mt][t + 1][2 * e + 1]);
+                            v.x *= w[mt][e], v.y *= w[mt][e], v.z *= w[mt][e], v.w *= w[mt][e];
+                            if (add) {
+                                const float4 u = *d;
+                                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                            }
+                            *d = v;
+                        } else {
+                            float2* d = reinterpret_cast<float2*>(row + 8 * t + 2 * qc);
+                            float2 v = make_float2(o[mt][t][2 * e] * w[mt][e], o[mt][t][2 * e + 1] * w[mt][e]);
+                            if (add) {
+                                const float2 u = *d;
+                                v.x += u.x, v.y += u.y;
+                            }
+                            *d = v;
+                        }
+                    }
+        };
+        if (warp < 2) place(false, warp);
+        warps_sync();
+        if (warp >= 2) place(true, warp - 2);
+        warps_sync();
+        // ---- the output, or the range's partial sums
+        const bool whole = f.first && f.last;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
+        for (int i = threadIdx.x; i < kRows * (kDim / 8); i += 32 * kWarps) {
+            // the output's chunks run along a row, the partial sums' along the rows
+            const int r = whole ? i / (kDim / 8) : i % kRows, c = whole ? i % (kDim / 8) : i / kRows;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm.ml[k][r][0]);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) L += M == -INFINITY ? 0.0f : sm.ml[k][r][1] * ex2(sm.ml[k][r][0] - M);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(&sm.red[0][r][8 * c + e]);
+                const float4 y = *reinterpret_cast<const float4*>(&sm.red[1][r][8 * c + e]);
+                v[e] = x.x + y.x, v[e + 1] = x.y + y.y, v[e + 2] = x.z + y.z, v[e + 3] = x.w + y.w;
+            }
+            if (whole) {
+                if (r >= f.rows) continue;
+                const int t = r / g, head = f.h * g + r - t * g;
+                const int64_t token = f.s.row0 + t;
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                uint32_t u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = L == 0.0f ? 0u : pack16(v[2 * e] * inv, v[2 * e + 1] * inv, kOutBf);
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs +
+                                          8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
+                if (a.lse && c == 0) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+            } else {
+                float4* po = parts.o + (slot * (kDim / 4) + 2 * c) * kRows + r;
+                po[0] = make_float4(v[0], v[1], v[2], v[3]);
+                po[kRows] = make_float4(v[4], v[5], v[6], v[7]);
+                if (c == 0) parts.ml[slot * kRows + r] = make_float2(M, L);
+            }
+        }
+        if (!whole && f.first && threadIdx.x == 0)
+            parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+        warps_sync();  // the buffers are free for the next item
+    }
+}
+
+template <int kDim, int kMode, int kMT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    k_kv_rows(const __grid_constant__ KvAttn a, const __grid_constant__ KvMaps maps, const __grid_constant__ KvPlan plan,
+              const __grid_constant__ KvParts parts) {
+    extern __shared__ uint8_t smem_raw[];
+    using S = Smem<kDim, kMode, kMT>;
+    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    static_assert(sizeof(KvPlanSmem) <= sizeof(sm.kv), "the plan's arrays lie in the ring");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], kWarps);
+        }
+        sm.abort = 0;
+        fence_mbar_init();
+        parts.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
+    }
+    int64_t per;
+    const Cursor<kMT> cur = kv_plan<16 * kMT, PAGE, kOver>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
+    __syncthreads();
+    if (threadIdx.x < 32 * kWarps) role_rows<kDim, kMode, kMT>(sm, a, parts, per, plan.g, cur);
+    else role_load<kDim, kMode, kMT>(sm, a, maps, plan.g, cur);
+    __syncwarp();
+    __syncthreads();
+    if (sm.abort && threadIdx.x == 0) atomicOr(a.c.status, CSA2_DEVERR_TIMEOUT);
+}
+
+template <int kDim, int kMode, int kMT>
+cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
+    using S = Smem<kDim, kMode, kMT>;
+    constexpr int kSmem = sizeof(S) + 1024;
+    static_assert(kCtasPerSm * (kSmem + 1024) <= 233472, "two CTAs an SM");
+    static_assert(S::kStages >= 2, "a ring");
+    KvMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
+    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode))
+        return cudaErrorInvalidValue;
+    KvPlan plan;
+    plan.g = a.H / a.c.kv_heads;
+    plan.grid = kCtasPerSm * device_sm_count();
+    plan.min_per = kMinPer;
+    const KvParts parts = kv_parts(a.ws, plan.grid, 16 * kMT, kDim);
+    static std::atomic<uint64_t> attr_done{0};
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_rows<kDim, kMode, kMT>), kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    k_kv_rows<kDim, kMode, kMT><<<plan.grid, kThreads, kSmem, st>>>(a, maps, plan, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
+    return launch_behind(k_kv_join<kDim, kOutBf>, dim3(plan.grid, 1), 128, st, a, parts, plan.g, 16 * kMT);
+}
+
+template <int kDim, int kMode>
+cudaError_t rows_mode(const KvAttn& a, cudaStream_t st) {
+    return kv_rows_tile(a.max_new, a.H / a.c.kv_heads) == 16 ? rows_as<kDim, kMode, 1>(a, st) : rows_as<kDim, kMode, 2>(a, st);
+}
+
+}  // namespace
+
+size_t kv_rows_workspace_bytes(int tile, int head_dim) {
+    return kv_parts_bytes(kCtasPerSm * device_sm_count(), tile, head_dim);
+}
+
+cudaError_t launch_kv_rows(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st) {
+    const bool e4m3 = kv_dtype == CSA2_KV_E4M3, bf = dtype == CSA2_DTYPE_BF16;
+    if (head_dim == 64)
+        return e4m3 ? (bf ? rows_mode<64, kE4m3Bf16>(a, st) : rows_mode<64, kE4m3F16>(a, st))
+                    : (bf ? rows_mode<64, kBf16>(a, st) : rows_mode<64, kF16>(a, st));
+    return e4m3 ? (bf ? rows_mode<128, kE4m3Bf16>(a, st) : rows_mode<128, kE4m3F16>(a, st))
+                : (bf ? rows_mode<128, kBf16>(a, st) : rows_mode<128, kF16>(a, st));
+}
+
+}  // namespace csa2
