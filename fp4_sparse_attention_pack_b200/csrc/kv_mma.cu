@@ -13,17 +13,19 @@
 // rescale of O is rare and the softmax warps do it themselves.  The tensor core
 // works on one tile while the softmax warps work on the other.
 //
-// One CTA per SM, 512 threads, the items' work split evenly (kv_plan.cuh):
+// One CTA per SM, 384 threads (512 for an E4M3 cache), the items' work split evenly
+// (kv_plan.cuh):
 //   warps 0-3, 4-7   softmax of tile 0 and 1: thread = row (TMEM lane); at the
 //                    item's end the output, or the partial sums;
-//   warp 8           issues the MMAs;
-//   warp 9           loads K and V blocks by TMA (16-bit caches): two pages of
+//   warp 8           issues the MMAs, a half of P's keys as they arrive;
+//   warp 9           (16-bit caches) loads K and V blocks by TMA: two pages of
 //                    64 rows, 64 channels a box, 128-byte swizzle;
-//   warps 12-15      load the queries of the next item while this one ends; for
-//                    an E4M3 cache they also load K and V and widen them to fp16
-//                    (exact).  Queries are then brought to fp16 as well: a bf16
-//                    row is scaled by a power of two that takes its largest
-//                    magnitude into [2^14, 2^15), undone in c.
+//   the last ones    load the queries of the next item while this one ends and
+//                    tell the others which item it is.  For an E4M3 cache they
+//                    also load K and V and widen them to fp16 (exact); queries
+//                    are then brought to fp16 as well: a bf16 row is scaled by a
+//                    power of two that takes its largest magnitude into
+//                    [2^14, 2^15), undone in c.
 // Rows of V that no row of the item sees (behind the last key, before the
 // window, on a page that is not loaded) are zeroed in shared memory, because
 // 0 x NaN would reach the sums; their scores are masked.
@@ -49,8 +51,16 @@ using namespace sm100;
 constexpr int kTile = 256;  // rows of an item
 constexpr int kBlk = 128;   // keys of a block
 constexpr int kOver = 2;    // an item's start and end, in blocks
-constexpr int kThreads = 512;
-constexpr int kWarpMma = 8, kWarpTma = 9, kWarpLoad = 12;
+constexpr int kWarpMma = 8, kWarpTma = 9;
+// The last warps load: two the queries of a 16-bit cache's call; the blocks of an
+// E4M3 cache are widened on the way, by seven.
+constexpr int load_warps(int mode) { return is_e4m3(mode) ? 7 : 2; }
+constexpr int threads_of(int mode) { return is_e4m3(mode) ? 512 : 384; }
+// Registers of a thread at launch, of a softmax thread and of the others.
+constexpr int regs_launch(int mode) { return is_e4m3(mode) ? 128 : 168; }
+constexpr int regs_softmax(int mode) { return is_e4m3(mode) ? 168 : 208; }
+constexpr int regs_other(int) { return 88; }
+constexpr int kMixEvery = 4;  // of so many pairs of exponentials one is a polynomial
 constexpr int kRing = 16;   // blocks whose masks of bad pages are kept
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // two of each, 128 columns apart
@@ -64,9 +74,11 @@ struct __align__(1024) Smem {
     uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_full[2][2], o_done[2];  // p_full: [tile][half of the keys]
     uint64_t tail;                              // the TMA of a V block that needs zeroing landed
     uint64_t drained;
+    uint64_t frag_full[2], frag_empty[2];
+    KvFrag frag[2];                             // this item and the next (rows = 0: no more)
     uint32_t tmem_base;
     int abort;
 };
@@ -116,7 +128,7 @@ struct Ring {
 // ---------------------------------------------------------------- MMA
 
 template <int kDim, int kMode>
-__device__ void role_mma(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor cur, uint32_t tb) {
+__device__ void role_mma(Smem<kDim, kMode>& sm, uint32_t tb) {
     using S = Smem<kDim, kMode>;
     constexpr uint32_t kFmt = kMode == kBf16 ? 1 : 0;
     const uint32_t idesc_s = idesc_f16(128, kBlk, kFmt, 0, 0);
@@ -126,8 +138,7 @@ __device__ void role_mma(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor c
     const uint64_t desc_k = smem_desc(sm.kv[0][0], 16, 1024, kLayoutSw128);
     const uint64_t desc_v = smem_desc(sm.kv[0][0], kBlk * 128, 1024, kLayoutSw128);
     Ring<S::kStages> ring;
-    uint32_t items = 0, np[2] = {0, 0};  // completed items; P hand-overs of each tile
-    KvFrag f;
+    uint32_t items = 0, np[2] = {0, 0};  // items with keys; P hand-overs of each tile
     auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
@@ -137,8 +148,13 @@ __device__ void role_mma(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor c
         }
         tc_commit_w(&sm.s_full[t]);
     };
-    while (cur.next(a, g, f)) {
+    for (uint32_t n = 0;; ++n) {
+        if (!wait_bar_warp(sm, &sm.frag_full[n & 1], (n >> 1) & 1)) return;
+        const KvFrag& f = sm.frag[n & 1];
         const int nb = f.f1 - f.f0, tiles = f.rows > 128 ? 2 : 1;
+        if (f.rows == 0) return;
+        __syncwarp();
+        mbar_arrive_w(&sm.frag_empty[n & 1]);
         if (nb == 0) continue;
         if (!wait_bar_warp(sm, &sm.q_full, items & 1)) return;
         ++items;
@@ -158,13 +174,17 @@ __device__ void role_mma(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor c
             if (!wait_bar_warp(sm, &sm.full[sv], pv)) return;
             if (more && !wait_bar_warp(sm, &sm.full[sk], pk)) return;
             for (int t = 0; t < tiles; ++t) {
-                if (!wait_bar_warp(sm, &sm.p_full[t], np[t] & 1)) return;
-                ++np[t];
-                tc_fence_after();
+                for (int half = 0; half < 2; ++half) {  // O_t += P_t V, as P arrives
+                    if (!wait_bar_warp(sm, &sm.p_full[t][half], np[t] & 1)) return;
+                    tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < kBlk / 16; ++i)  // O_t += P_t V
-                    tc_mma_f16_ta_w(tb + kColO + 128 * t, tb + kColS + 128 * t + 8 * i,
-                                    desc_v + ((sv * kStageBytes + 2048 * i) >> 4), idesc_o, j > 0 || i > 0);
+                    for (int i2 = 0; i2 < kBlk / 32; ++i2) {
+                        const int i = i2 + half * (kBlk / 32);
+                        tc_mma_f16_ta_w(tb + kColO + 128 * t, tb + kColS + 128 * t + 8 * i,
+                                        desc_v + ((sv * kStageBytes + 2048 * i) >> 4), idesc_o, j > 0 || i > 0);
+                    }
+                }
+                ++np[t];
                 // in order behind the MMAs that read P, which S overwrites
                 if (more) scores(t, sk);
                 else tc_commit_w(&sm.o_done[t]);
@@ -290,12 +310,24 @@ __device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
 template <int kDim, int kMode>
 __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor cur) {
     using S = Smem<kDim, kMode>;
-    const int tid = threadIdx.x - 32 * kWarpLoad;
+    constexpr int kLoaders = 32 * load_warps(kMode);
+    const int tid = threadIdx.x - (threads_of(kMode) - kLoaders);
     Ring<S::kStages> ring;
     uint32_t used = 0, items = 0, blocks = 0;
     const uint32_t inv_g = 65536u / g + 1;  // x / g = x * inv_g >> 16 for x < 256 + g
     KvFrag f;
-    while (cur.next(a, g, f)) {
+    for (uint32_t n = 0;; ++n) {
+        const bool more = cur.next(a, g, f);
+        if (tid < 32) {  // the first loader warp tells the others which item is next
+            if (n > 1 && !wait_bar_warp(sm, &sm.frag_empty[n & 1], ((n >> 1) - 1) & 1)) return;
+            if (tid == 0) {
+                if (!more) f.rows = 0;
+                sm.frag[n & 1] = f;
+                mbar_arrive(&sm.frag_full[n & 1]);
+            }
+            __syncwarp();
+        }
+        if (!more) return;
         if (f.f1 == f.f0) continue;
         // ---- queries
         if (items > 0 && !wait_bar_warp(sm, &sm.q_empty, (items - 1) & 1)) return;
@@ -304,27 +336,37 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) + (int64_t)(f.s.row0 + f.v.t0) * a.q.ts +
                             (int64_t)f.h * g * a.q.hs;
         const int rows = f.rows > 128 ? 256 : 128;
-        const int c = tid % kChunks;
-        for (int r0 = tid / kChunks; r0 < rows; r0 += 4 * (128 / kChunks)) {
-            uint4 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = r0 + k * (128 / kChunks);
+        if constexpr (kMode != kE4m3Bf16) {
+            for (int i = tid; i < rows * kChunks; i += kLoaders) {
+                const int r = i / kChunks, c = i % kChunks;
                 const int x = rem0 + r, t = (x * inv_g) >> 16;
-                v[k] = make_uint4(0, 0, 0, 0);
-                if (r < f.rows)
-                    v[k] = *reinterpret_cast<const uint4*>(q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
+                uint8_t* dst = &sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)];
+                if (r < f.rows) cp_async16(dst, q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
+                else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+                if (kMode == kE4m3F16 && c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e, FLT_MIN);
             }
+            cp_async_commit();
+            cp_async_wait_all();
+        } else {
+            for (int i0 = tid; i0 < rows * kChunks; i0 += 4 * kLoaders) {  // rows * kChunks and kLoaders: whole warps
+                uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = r0 + k * (128 / kChunks);
-                if constexpr (kMode == kE4m3Bf16) {
-                    const float k2 = scale_row<kChunks>(v[k], fmaxf(a.scale * kLog2e, FLT_MIN));
-                    if (c == 0) sm.qc[items & 1][r] = k2;
-                } else if constexpr (kMode == kE4m3F16) {
-                    if (c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e, FLT_MIN);
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * kLoaders, r = i / kChunks, c = i % kChunks;
+                    const int x = rem0 + r, t = (x * inv_g) >> 16;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (r < f.rows)
+                        v[k] = *reinterpret_cast<const uint4*>(q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
                 }
-                *reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)]) = v[k];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * kLoaders, r = i / kChunks, c = i % kChunks;
+                    const float k2 = scale_row<kChunks>(v[k], fmaxf(a.scale * kLog2e, FLT_MIN));
+                    if (r < rows) {
+                        if (c == 0) sm.qc[items & 1][r] = k2;
+                        *reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)]) = v[k];
+                    }
+                }
             }
         }
         fence_proxy_async_smem();
@@ -332,46 +374,67 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         mbar_arrive_w(&sm.q_full);
         ++items;
         if constexpr (is_e4m3(kMode)) {
-            // ---- K and V: a thread's 16 channels of rows r0, r0 + kStep, ...
-            constexpr int kCh = kDim / 16, kStep = 128 / kCh, kN = kBlk / kStep;
-            const int c16 = tid % kCh, r0 = tid / kCh;
+            // ---- K and V: chunks of 16 channels, kLoaders apart; a block is taken in
+            // parts, each part's loads in flight while the part before is widened
+            constexpr int kCh = kDim / 16, kAll = kBlk * kCh, kPart = 3;
             const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
-            for (int j = f.f0; j < f.f1; ++j, ++blocks) {
-                const int last = f.v.hi / PAGE, first = f.v.lo / PAGE;
-                const PagePair pp = pages_of(a, f, j, 2 * j >= first && 2 * j <= last ? table[2 * j] : -1,
-                                             2 * j + 1 >= first && 2 * j + 1 <= last ? table[2 * j + 1] : -1);
-                if (pp.bad && tid == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
-                uint4 v[2][kN];
+            const int last = f.v.hi / PAGE, first = f.v.lo / PAGE;
+            auto ids = [&](int j) {
+                return pages_of(a, f, j, 2 * j >= first && 2 * j <= last ? table[2 * j] : -1,
+                                2 * j + 1 >= first && 2 * j + 1 <= last ? table[2 * j + 1] : -1);
+            };
+            auto fetch = [&](const PagePair& pp, int j, bool is_v, int i0, uint4(&v)[kPart]) {
 #pragma unroll
-                for (int is_v = 0; is_v < 2; ++is_v)
-#pragma unroll
-                    for (int k = 0; k < kN; ++k) {
-                        const int r = r0 + k * kStep, p = r < 64 ? pp.p[0] : pp.p[1];
-                        v[is_v][k] = make_uint4(0, 0, 0, 0);
-                        if (p >= 0 && !(is_v && v_row_unseen(f, pp, j, r)))
-                            v[is_v][k] = *reinterpret_cast<const uint4*>(
-                                (is_v ? a.c.v : a.c.k) + (((int64_t)p * a.c.kv_heads + f.h) * PAGE + (r & 63)) * kDim + 16 * c16);
-                    }
-#pragma unroll
-                for (int is_v = 0; is_v < 2; ++is_v) {
-                    if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
-                    ++used;
-                    if (!is_v && tid == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
-#pragma unroll
-                    for (int k = 0; k < kN; ++k) {
-                        const int r = r0 + k * kStep;
-                        uint4 lo, hi;
-                        widen16(v[is_v][k], lo, hi);
-                        uint8_t* slab = sm.kv[ring.i][c16 >> 2];
-                        const int ch = 2 * (c16 & 3);
-                        *reinterpret_cast<uint4*>(slab + sw128(r, ch)) = lo;
-                        *reinterpret_cast<uint4*>(slab + sw128(r, ch + 1)) = hi;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    mbar_arrive_w(&sm.full[ring.i]);
-                    ring.step();
+                for (int k = 0; k < kPart; ++k) {
+                    const int i = i0 + k * kLoaders, r = i / kCh, c16 = i % kCh, p = r < 64 ? pp.p[0] : pp.p[1];
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (i < kAll && p >= 0 && !(is_v && v_row_unseen(f, pp, j, r)))
+                        v[k] = *reinterpret_cast<const uint4*>(
+                            (is_v ? a.c.v : a.c.k) + (((int64_t)p * a.c.kv_heads + f.h) * PAGE + (r & 63)) * kDim + 16 * c16);
                 }
+            };
+            auto put = [&](int i0, const uint4(&v)[kPart]) {
+#pragma unroll
+                for (int k = 0; k < kPart; ++k) {
+                    const int i = i0 + k * kLoaders, r = i / kCh, c16 = i % kCh;
+                    if (i >= kAll) continue;
+                    uint4 lo, hi;
+                    widen16(v[k], lo, hi);
+                    uint8_t* slab = sm.kv[ring.i][c16 >> 2];
+                    const int ch = 2 * (c16 & 3);
+                    *reinterpret_cast<uint4*>(slab + sw128(r, ch)) = lo;
+                    *reinterpret_cast<uint4*>(slab + sw128(r, ch + 1)) = hi;
+                }
+            };
+            PagePair pp = ids(f.f0);
+            uint4 v[2][kPart];
+            constexpr int kParts = (kAll + kPart * kLoaders - 1) / (kPart * kLoaders);
+            fetch(pp, f.f0, false, tid, v[0]);
+#pragma unroll 1
+            for (int j = f.f0; j < f.f1; ++j, ++blocks) {
+                PagePair next = pp;
+                if (pp.bad && tid == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+                if (j + 1 < f.f1) next = ids(j + 1);
+#pragma unroll
+                for (int x = 0; x < 2 * kParts; ++x) {  // parts of K, then of V
+                    const bool is_v = x >= kParts;
+                    const int part = x % kParts, y = x + 1;
+                    if (y < 2 * kParts) fetch(pp, j, y >= kParts, tid + (y % kParts) * kPart * kLoaders, v[y & 1]);
+                    else if (j + 1 < f.f1) fetch(next, j + 1, false, tid, v[y & 1]);
+                    if (part == 0) {
+                        if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
+                        ++used;
+                        if (!is_v && tid == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
+                    }
+                    put(tid + part * kPart * kLoaders, v[x & 1]);
+                    if (part + 1 == kParts) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        mbar_arrive_w(&sm.full[ring.i]);
+                        ring.step();
+                    }
+                }
+                pp = next;
             }
         }
     }
@@ -379,149 +442,199 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
 
 // ---------------------------------------------------------------- softmax
 
+// 2^t of two values in fp32 arithmetic, for t in [-126, 2^22): t = n + f with
+// |f| <= 1/2, a polynomial for 2^f (the minimax one of degree 4, computed for
+// this file by Remez exchange: relative error 2.6e-6, far below the rounding to
+// 16 bits) and n added to the exponent.  Below -126 the value is that of -126;
+// NaN gives a huge value, so that the row's result is not finite.
+__device__ __forceinline__ float2 ex2_poly(float2 t) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(-126.0f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(-126.0f));
+    constexpr float kRound = 12582912.0f;  // 1.5 x 2^23: the sum's low bits are n
+    const float2 r = add2(t, splat2(kRound));
+    const float2 f = sub2(t, sub2(r, splat2(kRound)));
+    float2 p = fma2(splat2(9.570101912e-3f), f, splat2(5.591786032e-2f));
+    p = fma2(p, f, splat2(0.2402474483f));
+    p = fma2(p, f, splat2(0.6931218147f));
+    p = fma2(p, f, splat2(0.9999992614f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(r.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
+}
+
+// P of 32 keys, 2^(c s - m), in 16 bits, and its sums.  kMix: some pairs by
+// polynomial, as the special-function units (16 values a clock) would bound the
+// kernel otherwise; without it masked scores give exact zeros.
+template <bool kMix, bool kBf>
+__device__ __forceinline__ void exps(const uint32_t (&s)[32], float2 c, float2 m, float2 (&sum)[2], uint32_t (&p)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float2 e = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c, m);
+        if (kMix && i % kMixEvery == kMixEvery - 1) e = ex2_poly(e);
+        else e = make_float2(ex2(e.x), ex2(e.y));
+        sum[i & 1] = add2(sum[i & 1], e);
+        p[i] = pack16(e.x, e.y, kBf);
+    }
+}
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+    float m[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+    for (int i = 2; i < 30; i += 4) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) m[k] = fmaxf(fmaxf(m[k], __uint_as_float(x[i + 2 * k])), __uint_as_float(x[i + 2 * k + 1]));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+}
+
 template <int kDim, int kMode>
-__device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, Cursor cur,
-                             uint32_t tb) {
+__device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, uint32_t tb) {
     const int t = threadIdx.x >> 7, row = threadIdx.x & 127;  // tile; row = TMEM lane
     const uint32_t lane_base = tb + ((uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16);
     const uint32_t ts = lane_base + kColS + 128 * t, to = lane_base + kColO + 128 * t;
     constexpr bool kP16Bf = kMode == kBf16;  // P in V's type
     constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
     uint32_t ns = 0, no = 0, items = 0, blocks = 0;
-    KvFrag f;
-    while (cur.next(a, g, f)) {
+    for (uint32_t n = 0;; ++n) {
+        if (!wait_bar_warp(sm, &sm.frag_full[n & 1], (n >> 1) & 1)) return;
+        const KvFrag& f = sm.frag[n & 1];
+        if (f.rows == 0) return;
         const int nb = f.f1 - f.f0;
         const int it = items;
         if (nb > 0) ++items;
         const int blk0 = blocks;
         blocks += nb;
-        if (f.rows <= 128 * t) continue;
-        const int x = min(f.tile * kTile - f.v.t0 * g + 128 * t + row, f.tile * kTile - f.v.t0 * g + f.rows - 1);
-        const int tok = f.v.t0 + x / g, hd = x % g;
-        const int pos = f.s.n - f.s.m + tok;                        // the row sees keys lo .. pos
-        const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        float mref = -INFINITY, l = 0.0f;
-        float c = fmaxf(a.scale * kLog2e, FLT_MIN);  // never 0: a masked score is -infinity
-        for (int j = f.f0; j < f.f1; ++j) {
-            if (!wait_bar_warp(sm, &sm.s_full[t], ns & 1)) return;
-            ++ns;
-            __syncwarp();
-            tc_fence_after();
-            if constexpr (is_e4m3(kMode)) {
-                if (j == f.f0) c = sm.qc[it & 1][128 * t + row];
-            }
-            float s[128];
+        if (f.rows > 128 * t) {
+            int pos, lo;  // the row sees keys lo .. pos
             {
-                uint32_t r0[32], r1[32], r2[32], r3[32];
-                tmem_ld_x32_nowait(ts, r0);
-                tmem_ld_x32_nowait(ts + 32, r1);
-                tmem_ld_x32_nowait(ts + 64, r2);
-                tmem_ld_x32_nowait(ts + 96, r3);
-                tmem_wait_ld2(r0, r1);
-                tmem_wait_ld2(r2, r3);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    s[i] = __uint_as_float(r0[i]);
-                    s[32 + i] = __uint_as_float(r1[i]);
-                    s[64 + i] = __uint_as_float(r2[i]);
-                    s[96 + i] = __uint_as_float(r3[i]);
+                const int x = min(f.tile * kTile - f.v.t0 * g + 128 * t + row, f.tile * kTile - f.v.t0 * g + f.rows - 1);
+                pos = f.s.n - f.s.m + f.v.t0 + x / g;
+                lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            }
+            float mref = -INFINITY, l = 0.0f;
+            float c = fmaxf(a.scale * kLog2e, FLT_MIN);  // never 0: a masked score is -infinity
+            const int j0 = f.f0, j1 = f.f1;
+            for (int j = j0; j < j1; ++j) {
+                if (!wait_bar_warp(sm, &sm.s_full[t], ns & 1)) return;
+                ++ns;
+                __syncwarp();
+                tc_fence_after();
+                if constexpr (is_e4m3(kMode)) {
+                    if (j == j0) c = sm.qc[it & 1][128 * t + row];
                 }
-            }
-            const int bad = sm.bad[(blk0 + j - f.f0) % kRing];
-            const int c_hi = pos - j * kBlk, c_lo = lo - j * kBlk;
-            if (__any_sync(0xffffffffu, c_hi < kBlk - 1 || c_lo > 0) || bad) {
+                uint32_t r[4][32];
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > c_hi || i < c_lo || (bad & (i < 64 ? 1 : 2))) s[i] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+                for (int k = 0; k < 4; ++k) tmem_ld_x32_nowait(ts + 32 * k, r[k]);
+                const int bad = sm.bad[(blk0 + j - j0) % kRing], k0 = j * kBlk;
+                const bool part = __any_sync(0xffffffffu, pos - k0 < kBlk - 1 || lo - k0 > 0) || bad;
+                auto masked = [&](int k, uint32_t(&x)[32]) {
+                    const int c_hi = bad >> (k >> 1) & 1 ? -1 : pos - k0 - 32 * k, c_lo = lo - k0 - 32 * k;
 #pragma unroll
-            for (int i = 4; i < 128; i += 8) {
+                    for (int i = 0; i < 32; ++i)
+                        if (i > c_hi || i < c_lo) x[i] = 0xFF800000u;  // -infinity
+                };
+                tmem_wait_ld2(r[0], r[1]);
+                tmem_wait_ld2(r[2], r[3]);
+                if (part) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = i + 4 + k < 128 ? fmaxf(fmaxf(mx[k], s[i + k]), s[i + 4 + k]) : fmaxf(mx[k], s[i + k]);
-            }
-            const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool move = bm > mref + kGap || (mref == -INFINITY && bm > -INFINITY);
-            if (__any_sync(0xffffffffu, move)) {
-                const float f1 = move ? ex2(mref - bm) : 1.0f;  // mref = -inf: 0
-                if (move) mref = bm;
-                l *= f1;
-                if (j > f.f0) {  // O holds the blocks before
+                    for (int k = 0; k < 4; ++k) masked(k, r[k]);
+                }
+                const float bm = fmaxf(fmaxf(max32(r[0]), max32(r[1])), fmaxf(max32(r[2]), max32(r[3]))) * c;
+                const bool move = bm > mref + kGap || (mref == -INFINITY && bm > -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f1 = move ? ex2(mref - bm) : 1.0f;  // mref = -inf: 0
+                    if (move) mref = bm;
+                    l *= f1;
+                    if (j > j0) {  // O holds the blocks before
 #pragma unroll 1
-                    for (int k = 0; k < kDim; k += 16) {
-                        float o[16];
-                        tmem_ld_32x32b_x16(to + k, o);
+                        for (int k = 0; k < kDim; k += 16) {
+                            float o[16];
+                            tmem_ld_32x32b_x16(to + k, o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= f1;
-                        tmem_st_32x32b_x16(to + k, o);
+                            for (int i = 0; i < 16; ++i) o[i] *= f1;
+                            tmem_st_32x32b_x16(to + k, o);
+                        }
                     }
                 }
-            }
-            const float ms = mref == -INFINITY ? 0.0f : mref;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            float p[64];  // two 16-bit values each
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                const float e0 = ex2(fmaf(s[2 * i], c, -ms)), e1 = ex2(fmaf(s[2 * i + 1], c, -ms));
-                sum[(2 * i) & 3] += e0;
-                sum[(2 * i + 1) & 3] += e1;
-                p[i] = __uint_as_float(pack16(e0, e1, kP16Bf));
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_32x32b_x64(ts, p);
-            tc_fence_before();
-            __syncwarp();
-            mbar_arrive_w(&sm.p_full[t]);
-        }
-        // ---- the item's end
-        if (nb > 0) {
-            if (!wait_bar_warp(sm, &sm.o_done[t], no & 1)) return;
-            ++no;
-            __syncwarp();
-            tc_fence_after();
-        }
-        const bool mine = 128 * t + row < f.rows;
-        if (f.first && f.last) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int64_t token = f.s.row0 + tok;
-            const int head = f.h * g + hd;
-            uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
+                const float2 c2 = splat2(c), m2 = splat2(mref == -INFINITY ? 0.0f : -mref);
+                float2 sum[2] = {make_float2(l, 0.f), splat2(0.f)};
+                // 64 keys at a time, their scores read again: a short loop and few registers
+                // (one pass over 128 scores in registers took 4% longer, one over 32 10%)
 #pragma unroll 1
-            for (int k = 0; k < kDim; k += 32) {
-                float o[32];
-                if (nb > 0) tmem_ld_32x32b_x32(to + k, o);
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv, kOutBf);
-                    if (mine) *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[16];
+                    tmem_ld_x32_nowait(ts + 64 * h, r[0]);
+                    tmem_ld_x32_nowait(ts + 64 * h + 32, r[1]);
+                    tmem_wait_ld2(r[0], r[1]);
+                    if (part) {
+                        masked(2 * h, r[0]);
+                        exps<false, kP16Bf>(r[0], c2, m2, sum, p);
+                        tmem_st_x16_nowait(ts + 32 * h, p);
+                        masked(2 * h + 1, r[1]);
+                        exps<false, kP16Bf>(r[1], c2, m2, sum, p);
+                    } else {
+                        exps<true, kP16Bf>(r[0], c2, m2, sum, p);
+                        tmem_st_x16_nowait(ts + 32 * h, p);
+                        exps<true, kP16Bf>(r[1], c2, m2, sum, p);
+                    }
+                    tmem_st_x16_nowait(ts + 32 * h + 16, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_w(&sm.p_full[t][h]);  // the product with these keys' values begins
                 }
+                l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            if (mine && a.lse) a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
-        } else {
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
-            float4* po = parts.o + slot * (kDim / 4) * kTile + 128 * t + row;
+            // ---- the item's end
+            if (nb > 0) {
+                if (!wait_bar_warp(sm, &sm.o_done[t], no & 1)) return;
+                ++no;
+                __syncwarp();
+                tc_fence_after();
+            }
+            const bool mine = 128 * t + row < f.rows;
+            if (f.first && f.last) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int x = f.tile * kTile - f.v.t0 * g + min(128 * t + row, f.rows - 1);
+                const int64_t token = f.s.row0 + f.v.t0 + x / g;
+                const int head = f.h * g + x % g;
+                uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
 #pragma unroll 1
-            for (int k = 0; k < kDim; k += 32) {
-                float o[32];
-                tmem_ld_32x32b_x32(to + k, o);
+                for (int k = 0; k < kDim; k += 32) {
+                    float o[32];
+                    if (nb > 0) tmem_ld_32x32b_x32(to + k, o);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv, kOutBf);
+                        if (mine) *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (mine && a.lse) a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
+            } else {
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
+                float4* po = parts.o + slot * (kDim / 4) * kTile + 128 * t + row;
+#pragma unroll 1
+                for (int k = 0; k < kDim; k += 32) {
+                    float o[32];
+                    tmem_ld_32x32b_x32(to + k, o);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+                parts.ml[slot * kTile + 128 * t + row] = make_float2(mref, l);
+                if (f.first && threadIdx.x == 0)
+                    parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
             }
-            parts.ml[slot * kTile + 128 * t + row] = make_float2(mref, l);
-            if (f.first && threadIdx.x == 0)
-                parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+            tc_fence_before();
         }
-        tc_fence_before();
         __syncwarp();
+        mbar_arrive_w(&sm.frag_empty[n & 1]);
     }
 }
 
 template <int kDim, int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kMode), 1)
     k_kv_mma(const __grid_constant__ KvAttn a, const __grid_constant__ KvMaps maps, const __grid_constant__ KvPlan plan,
              const __grid_constant__ KvParts parts) {
     extern __shared__ uint8_t smem_raw[];
@@ -531,14 +644,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&sm.full[i], is_e4m3(kMode) ? 4 : 1);
+            mbar_init(&sm.full[i], is_e4m3(kMode) ? load_warps(kMode) : 1);
             mbar_init(&sm.empty[i], 1);
         }
-        mbar_init(&sm.q_full, 4);
+        mbar_init(&sm.q_full, load_warps(kMode));
         mbar_init(&sm.q_empty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
-            mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.p_full[t][0], 4);
+            mbar_init(&sm.p_full[t][1], 4);
+            mbar_init(&sm.frag_full[t], 1);
+            mbar_init(&sm.frag_empty[t], 9);
             mbar_init(&sm.o_done[t], 1);
         }
         mbar_init(&sm.tail, 1);
@@ -555,15 +671,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
-    // 128 registers a thread at launch; the softmax warps take what the others give up
+    // the softmax warps take the registers that the others give up
+    static_assert(threads_of(kMode) * regs_launch(kMode) <= 65536 &&
+                      256 * regs_softmax(kMode) + (threads_of(kMode) - 256) * regs_other(kMode) <=
+                          threads_of(kMode) * regs_launch(kMode),
+                  "more registers than the block was launched with");
     if (warp < 8) {
-        regs_up<176>();
-        role_softmax<kDim, kMode>(sm, a, parts, per, plan.g, cur, tb);
+        regs_up<regs_softmax(kMode)>();
+        role_softmax<kDim, kMode>(sm, a, parts, per, plan.g, tb);
     } else {
-        regs_down<80>();
-        if (warp == kWarpMma) role_mma<kDim, kMode>(sm, a, plan.g, cur, tb);
+        regs_down<regs_other(kMode)>();
+        if (warp == kWarpMma) role_mma<kDim, kMode>(sm, tb);
         else if (warp == kWarpTma && !is_e4m3(kMode)) role_tma<kDim, kMode>(sm, a, maps, plan.g, cur);
-        else if (warp >= kWarpLoad) role_load<kDim, kMode>(sm, a, plan.g, cur);
+        else role_load<kDim, kMode>(sm, a, plan.g, cur);
     }
     __syncwarp();
     __syncthreads();
@@ -600,7 +720,7 @@ cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     static std::atomic<uint64_t> attr_done{0};
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_mma<kDim, kMode>), kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    k_kv_mma<kDim, kMode><<<plan.grid, kThreads, kSmem, st>>>(a, maps, plan, parts);
+    k_kv_mma<kDim, kMode><<<plan.grid, threads_of(kMode), kSmem, st>>>(a, maps, plan, parts);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     constexpr bool kBf = kMode == kBf16 || kMode == kE4m3Bf16;
