@@ -95,7 +95,7 @@ int csa2_rotate(const csa2_rotary* rot, const csa2_heads* x, const csa2_heads* y
     int rc = check_rotary(rot, head_dim);
     if (rc) return rc;
     if (n_tokens == 0) return CSA2_OK;
-    if (n_tokens > (int64_t)1 << 30 || n_tokens * heads > (int64_t)1 << 40) return CSA2_ERR_UNSUPPORTED;
+    if (n_tokens > (int64_t)1 << 30 || heads > CSA2_ROTATE_MAX_HEADS) return CSA2_ERR_UNSUPPORTED;
     if ((rc = check_heads(x, n_tokens, heads, head_dim, false)) || (rc = check_heads(y, n_tokens, heads, head_dim, true)))
         return rc;
     if (!pos) return CSA2_ERR_INVALID_ARG;
@@ -159,7 +159,7 @@ int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dty
         H % cache->kv_heads || !std::isfinite(scale) || scale <= 0.0f || !cu)
         return CSA2_ERR_INVALID_ARG;
     if ((int64_t)total * H > ((int64_t)1 << 31) - 4096) return CSA2_ERR_UNSUPPORTED;  // rows are counted in 32 bits
-    if (total == 0 || max_new == 0) return CSA2_OK;
+    if (total == 0) return CSA2_OK;
     if ((rc = check_heads(q, total, H, cache->head_dim, false)) || (rc = check_heads(out, total, H, cache->head_dim, true)))
         return rc;
     if (q->data == out->data) return CSA2_ERR_INVALID_ARG;

@@ -11,7 +11,9 @@
 // Both kernels are bound by memory (large calls) or by latency (a decode step).
 // A thread's unit of work is 8 channels of a row, or 8 + 8 when the pair's two
 // channels are half a rotation apart, so every access is 16 bytes (8 for the
-// write of E4M3 codes) and a warp covers whole lines.
+// write of E4M3 codes) and a warp covers whole lines.  A thread has at most four
+// units and loads all of them before it looks up positions, slots and pages and
+// computes the angles, so those chains of small loads lie under the large ones.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -21,6 +23,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
+template <typename In>
+constexpr int kUnits = sizeof(In) == 4 ? 2 : 4;  // units of a thread
 
 template <typename T>
 struct Vec8;  // 8 channels as they lie in memory
@@ -103,61 +107,94 @@ __device__ __forceinline__ void store8(T* p, const Vec8<T>& v) {
     *reinterpret_cast<Vec8<T>*>(p) = v;
 }
 
-// 8 channels unchanged but for the type.
 template <typename In, typename Out>
-__device__ __forceinline__ void copy8(const In* src, Out* dst) {
+__device__ __forceinline__ void convert8(const Vec8<In>& v, Vec8<Out>& o) {
     if constexpr (std::is_same<In, Out>::value) {
-        store8(dst, load8(src));
+        o = v;
     } else {
         float f[8];
-        Vec8<Out> o;
-        unpack(load8(src), f);
+        unpack(v, f);
         pack(f, o);
-        store8(dst, o);
     }
 }
 
 // Units of a row that rotate; the other channels are (dim - rot) / 8 more.
 __host__ __device__ __forceinline__ int rot_units(int rot, int neighbours) { return neighbours ? rot / 8 : rot / 16; }
 
-// Unit u of a row whose first R units rotate by cs (one (cos, sin) per pair).
+// Channels of a unit that does not rotate, the u-th such one of a row.
+__device__ __forceinline__ int other_channel(const RotaryView& r, int u) {
+    const int c = 8 * u;
+    return c >= r.offset ? c + r.rot : c;
+}
+template <typename In>
+struct Unit {
+    Vec8<In> a, b;  // b: the pairs' other channels, half a rotation behind
+};
+// Unit u of a row that rotates.
+template <typename In>
+__device__ __forceinline__ void load_turn(Unit<In>& x, const In* src, int u, const RotaryView& r) {
+    src += r.offset + 8 * u;
+    x.a = load8(src);
+    if (!r.neighbours) x.b = load8(src + r.rot / 2);
+}
 template <typename In, typename Out>
-__device__ __forceinline__ void row_unit(const In* src, Out* dst, int u, int R, const RotaryView& r, const float2* cs) {
-    if (u >= R) {
-        int c = 8 * (u - R);
-        if (c >= r.offset) c += r.rot;
-        copy8(src + c, dst + c);
-    } else if (r.neighbours) {
-        const int c = r.offset + 8 * u;
-        float f[8], g[8];
-        unpack(load8(src + c), f);
+__device__ __forceinline__ void store_turn(const Unit<In>& v, Out* dst, int u, const RotaryView& r, const float2* cs) {
+    Vec8<Out> o;
+    float a[8], x[8];
+    dst += r.offset + 8 * u;
+    unpack(v.a, a);
+    if (r.neighbours) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 w = cs[4 * u + i];
-            g[2 * i] = f[2 * i] * w.x - f[2 * i + 1] * w.y;
-            g[2 * i + 1] = f[2 * i + 1] * w.x + f[2 * i] * w.y;
+            const float2 w = cs[u + i * (r.rot / 8)];
+            x[2 * i] = a[2 * i] * w.x - a[2 * i + 1] * w.y;
+            x[2 * i + 1] = a[2 * i + 1] * w.x + a[2 * i] * w.y;
         }
-        Vec8<Out> o;
-        pack(g, o);
-        store8(dst + c, o);
     } else {
-        const int c = r.offset + 8 * u, h = r.rot / 2;
-        float a[8], b[8], x[8], y[8];
-        const Vec8<In> va = load8(src + c), vb = load8(src + c + h);
-        unpack(va, a);
-        unpack(vb, b);
+        float b[8], y[8];
+        unpack(v.b, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 w = cs[8 * u + i];
+            const float2 w = cs[u + i * (r.rot / 16)];
             x[i] = a[i] * w.x - b[i] * w.y;
             y[i] = b[i] * w.x + a[i] * w.y;
         }
-        Vec8<Out> o;
-        pack(x, o);
-        store8(dst + c, o);
         pack(y, o);
-        store8(dst + c + h, o);
+        store8(dst + r.rot / 2, o);
     }
+    pack(x, o);
+    store8(dst, o);
+}
+
+// Division of x < 2^16 by d < 2^16: m = 2^32 / d + 1 (0 for d = 1).
+struct Divisor {
+    uint32_t d, m;
+};
+__device__ __forceinline__ int divide(int x, const Divisor& v) { return v.m ? (int)__umulhi((uint32_t)x, v.m) : x; }
+__host__ __device__ __forceinline__ Divisor divisor(int d) {
+    return {(uint32_t)d, d > 1 ? 0xFFFFFFFFu / (uint32_t)d + 1 : 0};
+}
+
+// The units of a CTA's rows, kind after kind, so that a warp's are nearly always
+// of one kind: those that rotate, the other channels of the same rows, and (an
+// append) the values'.
+struct Kinds {
+    Divisor turn, other, value;  // units of a row
+};
+struct Where {
+    uint32_t bits;  // the unit of the row 0-7, head 8-18, token 19-25, kind 26-27
+    __device__ __forceinline__ int u() const { return bits & 0xFF; }
+    __device__ __forceinline__ int h() const { return bits >> 8 & 0x7FF; }
+    __device__ __forceinline__ int t() const { return bits >> 19 & 0x7F; }
+    __device__ __forceinline__ int kind() const { return bits >> 26; }
+};
+__device__ __forceinline__ Where where(int i, int nt, int nh, const Divisor& per_token, const Kinds& k) {
+    const int n0 = nt * nh * k.turn.d, n1 = nt * nh * k.other.d;
+    const int kind = i < n0 ? 0 : i < n0 + n1 ? 1 : 2;
+    const Divisor& v = kind == 0 ? k.turn : kind == 1 ? k.other : k.value;
+    i -= kind == 0 ? 0 : kind == 1 ? n0 : n0 + n1;
+    const int row = divide(i, v), t = divide(row, per_token);
+    return {(uint32_t)(i - row * (int)v.d) | (uint32_t)(row - t * nh) << 8 | (uint32_t)t << 19 | (uint32_t)kind << 26};
 }
 
 // (cos, sin) of pair i at a position.
@@ -170,29 +207,48 @@ __device__ __forceinline__ float2 turn_of(const RotaryView& r, int i, int positi
     return make_float2(c, r.sign * s);
 }
 
+// Place of a token's pair p in shared memory: neighbouring units' (cos, sin) side
+// by side, so that a warp reads them without bank conflicts.
+__device__ __forceinline__ int cs_at(const RotaryView& r, int p) {
+    return r.neighbours ? (p >> 2) + (p & 3) * (r.rot / 8) : (p >> 3) + (p & 7) * (r.rot / 16);
+}
+
 __device__ __forceinline__ int axis_of(const RotaryView& r, int i) { return (r.axis[i / 16] >> (2 * (i % 16))) & 3; }
 
-// Rows of `tt` tokens x `ht` heads a CTA: blockIdx.x tokens, blockIdx.y heads.
+// `tt` tokens (blockIdx.x) x `ht` heads (blockIdx.y) a CTA.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_rotate(const __grid_constant__ RotaryView r, HeadsView x, HeadsView y,
-                                                     int64_t n_tokens, int heads, int tt, int ht, int units) {
+                                                     int64_t n_tokens, int heads, int tt, int ht, Kinds kinds,
+                                                     Divisor pairs) {
     extern __shared__ float2 cs[];  // [tt][rot / 2]
     const int64_t t0 = (int64_t)blockIdx.x * tt;
     const int nt = (int)min((int64_t)tt, n_tokens - t0);
     const int h0 = blockIdx.y * ht, nh = min(ht, heads - h0);
-    const int half = r.rot / 2;
+    const int half = r.rot / 2, total = nt * nh * (int)(kinds.turn.d + kinds.other.d);
+    const Divisor per_token = divisor(nh);
+    Unit<T> v[kUnits<T>];
+    Where w[kUnits<T>];
+#pragma unroll
+    for (int k = 0; k < kUnits<T>; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= total) continue;
+        w[k] = where(i, nt, nh, per_token, kinds);
+        const T* src = reinterpret_cast<const T*>(x.p) + (t0 + w[k].t()) * x.ts + (h0 + w[k].h()) * x.hs;
+        if (w[k].kind() == 0) load_turn(v[k], src, w[k].u(), r);
+        else v[k].a = load8(src + other_channel(r, w[k].u()));
+    }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        cs[i] = turn_of(r, p, r.pos[axis_of(r, p) * r.pos_stride + t0 + t]);
+        const int t = divide(i, pairs), p = i - t * half;
+        cs[t * half + cs_at(r, p)] = turn_of(r, p, r.pos[axis_of(r, p) * r.pos_stride + t0 + t]);
     }
     __syncthreads();
-    const int R = rot_units(r.rot, r.neighbours);
-    for (int i = threadIdx.x; i < nt * nh * units; i += kThreads) {
-        const int row = i / units, u = i - row * units;
-        const int t = row / nh, h = row - t * nh;
-        const T* src = reinterpret_cast<const T*>(x.p) + (t0 + t) * x.ts + (h0 + h) * x.hs;
-        T* dst = reinterpret_cast<T*>(y.p) + (t0 + t) * y.ts + (h0 + h) * y.hs;
-        row_unit(src, dst, u, R, r, cs + t * half);
+#pragma unroll
+    for (int k = 0; k < kUnits<T>; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= total) continue;
+        T* dst = reinterpret_cast<T*>(y.p) + (t0 + w[k].t()) * y.ts + (h0 + w[k].h()) * y.hs;
+        if (w[k].kind() == 0) store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
+        else store8(dst + other_channel(r, w[k].u()), v[k].a);
     }
 }
 
@@ -231,7 +287,7 @@ __device__ __forceinline__ void count_tokens(const KvAppend& a, const int32_t* c
 template <typename In, typename Out>
 __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ KvAppend a,
                                                         const __grid_constant__ RotaryView r, int dim, int tt, int ht,
-                                                        int units_k) {
+                                                        Kinds kinds, Divisor pairs) {
     extern __shared__ float2 cs[];                                // [tt][rot / 2]
     const int half = r.rot / 2;
     int64_t* row = reinterpret_cast<int64_t*>(cs + tt * half);    // [tt] element of head 0 in the pools, or -1
@@ -239,6 +295,20 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
     int* cu = slot + tt;                                          // [batch + 1]
     const int t0 = blockIdx.x * tt, nt = min(tt, a.total - t0);
     const int h0 = blockIdx.y * ht, nh = min(ht, a.c.kv_heads - h0);
+    const int total = nt * nh * (int)(kinds.turn.d + kinds.other.d + kinds.value.d);
+    const Divisor per_token = divisor(nh);
+    Unit<In> v[kUnits<In>];
+    Where w[kUnits<In>];
+#pragma unroll
+    for (int k = 0; k < kUnits<In>; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= total) continue;
+        w[k] = where(i, nt, nh, per_token, kinds);
+        const HeadsView& x = w[k].kind() == 2 ? a.v : a.k;
+        const In* src = reinterpret_cast<const In*>(x.p) + (int64_t)(t0 + w[k].t()) * x.ts + (h0 + w[k].h()) * x.hs;
+        if (w[k].kind() == 0) load_turn(v[k], src, w[k].u(), r);
+        else v[k].a = load8(src + (w[k].kind() == 1 ? other_channel(r, w[k].u()) : 8 * w[k].u()));
+    }
     for (int i = threadIdx.x; i <= a.c.batch; i += kThreads) cu[i] = a.cu[i];
     __syncthreads();
     for (int i = threadIdx.x; i < nt; i += kThreads) {
@@ -262,24 +332,24 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
+        const int t = divide(i, pairs), p = i - t * half;
         if (row[t] >= 0)
-            cs[i] = turn_of(r, p, r.pos ? r.pos[axis_of(r, p) * r.pos_stride + t0 + t] : slot[t]);
+            cs[t * half + cs_at(r, p)] = turn_of(r, p, r.pos ? r.pos[axis_of(r, p) * r.pos_stride + t0 + t] : slot[t]);
     }
     __syncthreads();
-    const int R = rot_units(r.rot, r.neighbours), units = units_k + dim / 8;
-    for (int i = threadIdx.x; i < nt * nh * units; i += kThreads) {
-        const int rw = i / units, u = i - rw * units;
-        const int t = rw / nh, h = rw - t * nh + h0;
-        if (row[t] < 0) continue;
-        const int64_t at = row[t] + (int64_t)h * PAGE * dim;
-        if (u < units_k) {
-            row_unit(reinterpret_cast<const In*>(a.k.p) + (int64_t)(t0 + t) * a.k.ts + h * a.k.hs,
-                     reinterpret_cast<Out*>(a.c.k) + at, u, R, r, cs + t * half);
+#pragma unroll
+    for (int k = 0; k < kUnits<In>; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= total) continue;
+        const int64_t at = row[w[k].t()];
+        if (at < 0) continue;
+        Out* dst = reinterpret_cast<Out*>(w[k].kind() == 2 ? a.c.v : a.c.k) + at + (int64_t)(h0 + w[k].h()) * PAGE * dim;
+        if (w[k].kind() == 0) {
+            store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
         } else {
-            const int c = 8 * (u - units_k);
-            copy8(reinterpret_cast<const In*>(a.v.p) + (int64_t)(t0 + t) * a.v.ts + h * a.v.hs + c,
-                  reinterpret_cast<Out*>(a.c.v) + at + c);
+            Vec8<Out> o;
+            convert8(v[k].a, o);
+            store8(dst + (w[k].kind() == 1 ? other_channel(r, w[k].u()) : 8 * w[k].u()), o);
         }
     }
     if (a.start && blockIdx.x == 0 && blockIdx.y == 0) count_tokens(a, cu, threadIdx.x, kThreads);
@@ -290,15 +360,16 @@ __global__ void k_kv_count(const __grid_constant__ KvAppend a) {
     count_tokens(a, a.cu, threadIdx.x, blockDim.x);
 }
 
-// Tokens and heads of a CTA: about 2,048 units, fewer (down to one unit a
-// thread) while the CTAs would not fill the SMs twice.
-void tile_rows(int64_t tokens, int heads, int units, int half, int& tt, int& ht) {
+// Tokens and heads of a CTA: as many as its threads have units for, or fewer
+// (down to one unit a thread) while the CTAs would not fill the SMs twice.
+void tile_rows(int64_t tokens, int heads, int units, int half, int most, int& tt, int& ht) {
     const int64_t want = 2 * device_sm_count();
-    int per = 2048;
+    int per = most * kThreads;
     while (per > kThreads && tokens * heads * units / per < want) per /= 2;
-    ht = std::max(1, std::min(heads, per / units));
-    tt = ht < heads ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(per / (units * heads), 64));
-    tt = (int)std::min<int64_t>(tt, tokens);
+    const int parts = (heads * units + per - 1) / per;  // of a token's heads
+    ht = std::min((heads + parts - 1) / parts, per / units);
+    tt = ht < heads ? 1 : per / (units * heads);
+    tt = (int)std::min<int64_t>(std::min(tt, 64), tokens);
     if (half > 0) tt = std::min(tt, 4096 / half);  // 32 KB of (cos, sin)
 }
 
@@ -306,25 +377,27 @@ template <typename T>
 cudaError_t rotate_as(const RotaryView& r, const HeadsView& x, const HeadsView& y, int64_t n_tokens, int heads, int dim,
                       cudaStream_t st) {
     const bool in_place = x.p == y.p;  // the other channels are there already
-    const int units = rot_units(r.rot, r.neighbours) + (in_place ? 0 : (dim - r.rot) / 8);
+    const Kinds kinds = {divisor(rot_units(r.rot, r.neighbours)), divisor(in_place ? 0 : (dim - r.rot) / 8), divisor(0)};
+    const int units = kinds.turn.d + kinds.other.d;
     int tt, ht;
-    tile_rows(n_tokens, heads, units, r.rot / 2, tt, ht);
+    tile_rows(n_tokens, heads, units, r.rot / 2, kUnits<T>, tt, ht);
     const dim3 grid((unsigned)((n_tokens + tt - 1) / tt), (heads + ht - 1) / ht);
     k_rotate<T><<<grid, kThreads, (size_t)tt * (r.rot / 2) * sizeof(float2), st>>>(r, x, y, n_tokens, heads, tt, ht,
-                                                                                   units);
+                                                                                   kinds, divisor(r.rot / 2));
     return cudaGetLastError();
 }
 
 template <typename In, typename Out>
 cudaError_t append_as(const KvAppend& a, const RotaryView& r, int dim, cudaStream_t st) {
     if (a.total > 0) {
-        const int units_k = rot_units(r.rot, r.neighbours) + (dim - r.rot) / 8;
+        const Kinds kinds = {divisor(rot_units(r.rot, r.neighbours)), divisor((dim - r.rot) / 8), divisor(dim / 8)};
         int tt, ht;
-        tile_rows(a.total, a.c.kv_heads, units_k + dim / 8, r.rot / 2, tt, ht);
+        const int units = kinds.turn.d + kinds.other.d + kinds.value.d;
+        tile_rows(a.total, a.c.kv_heads, units, r.rot / 2, kUnits<In>, tt, ht);
         const dim3 grid((a.total + tt - 1) / tt, (a.c.kv_heads + ht - 1) / ht);
         const size_t smem = (size_t)tt * (r.rot / 2 * sizeof(float2) + sizeof(int64_t) + sizeof(int)) +
                             (size_t)(a.c.batch + 1) * sizeof(int);
-        k_kv_append<In, Out><<<grid, kThreads, smem, st>>>(a, r, dim, tt, ht, units_k);
+        k_kv_append<In, Out><<<grid, kThreads, smem, st>>>(a, r, dim, tt, ht, kinds, divisor(r.rot / 2));
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         if (a.start) return cudaSuccess;

@@ -523,7 +523,7 @@ typedef struct {
  * rot_dim is a multiple of 16 in 16..CSA2_MAX_ROT, rot_offset a multiple of 8,
  * n_axes 1..3 (CSA2_ERR_INVALID_ARG).
  */
-enum { CSA2_MAX_ROT = 256, CSA2_MAX_AXES = 3 };
+enum { CSA2_MAX_ROT = 256, CSA2_MAX_AXES = 3, CSA2_ROTATE_MAX_HEADS = 65535 };
 typedef struct {
     const float* inv_freq;
     const uint8_t* axis;
@@ -534,8 +534,9 @@ typedef struct {
 } csa2_rotary;
 
 /*
- * y = x with its channels rotated, for n_tokens tokens of `heads` heads of
- * head_dim channels (a multiple of 8, 8..512).  inverse = 1 turns by the
+ * y = x with its channels rotated, for n_tokens tokens (at most 2^30) of `heads`
+ * heads (at most CSA2_ROTATE_MAX_HEADS; CSA2_ERR_UNSUPPORTED beyond) of head_dim
+ * channels (a multiple of 8, 8..512).  inverse = 1 turns by the
  * negative angle, which undoes the rotation and is its backward pass (the
  * gradient of x is the inverse rotation of the gradient of y).  The other
  * channels are copied.  dtype (x and y): CSA2_DTYPE_BF16, _F16 or _F32.  pos is
