@@ -9,9 +9,9 @@
 // into shared memory and then streams its rows.
 //
 // Both kernels are bound by memory (large calls) or by latency (a decode step).
-// A thread's unit of work is 8 channels of a row, or 8 + 8 when the pair's two
-// channels are half a rotation apart, so every access is 16 bytes (8 for the
-// write of E4M3 codes) and a warp covers whole lines.  A thread has at most four
+// A thread's unit of work is 8 or 16 neighbouring channels of a row, or 8 + 8 when
+// the pair's two channels are half a rotation apart, so every access is 16 bytes
+// (8 for some writes of E4M3 codes) and a warp covers whole lines.  A thread has at most four
 // units and loads all of them before it looks up positions, slots and pages and
 // computes the angles, so those chains of small loads lie under the large ones.
 #include <algorithm>
@@ -121,15 +121,39 @@ __device__ __forceinline__ void convert8(const Vec8<In>& v, Vec8<Out>& o) {
 // Units of a row that rotate; the other channels are (dim - rot) / 8 more.
 __host__ __device__ __forceinline__ int rot_units(int rot, int neighbours) { return neighbours ? rot / 8 : rot / 16; }
 
-// Channels of a unit that does not rotate, the u-th such one of a row.
-__device__ __forceinline__ int other_channel(const RotaryView& r, int u) {
-    const int c = 8 * u;
+// First channel of a unit of `width` channels that does not rotate, the u-th such one of a row.
+__device__ __forceinline__ int other_channel(const RotaryView& r, int u, int width) {
+    const int c = width * u;
     return c >= r.offset ? c + r.rot : c;
 }
 template <typename In>
 struct Unit {
-    Vec8<In> a, b;  // b: the pairs' other channels, half a rotation behind
+    Vec8<In> a, b;  // b: the pairs' other channels, half a rotation behind, or the next 8
 };
+// Units that do not rotate: 8 channels, or 16.
+template <typename In>
+__device__ __forceinline__ void load_plain(Unit<In>& x, const In* src, int width) {
+    x.a = load8(src);
+    if (width == 16) x.b = load8(src + 8);
+}
+template <typename In, typename Out>
+__device__ __forceinline__ void store_plain(const Unit<In>& v, Out* dst, int width) {
+    Vec8<Out> o;
+    convert8(v.a, o);
+    if constexpr (sizeof(Out) == 1) {
+        if (width == 16) {
+            Vec8<Out> p;
+            convert8(v.b, p);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(o.a.x, o.a.y, p.a.x, p.a.y);
+            return;
+        }
+    }
+    store8(dst, o);
+    if (width == 16) {
+        convert8(v.b, o);
+        store8(dst + 8, o);
+    }
+}
 // Unit u of a row that rotates.
 template <typename In>
 __device__ __forceinline__ void load_turn(Unit<In>& x, const In* src, int u, const RotaryView& r) {
@@ -180,6 +204,7 @@ __host__ __device__ __forceinline__ Divisor divisor(int d) {
 // append) the values'.
 struct Kinds {
     Divisor turn, other, value;  // units of a row
+    int width;                   // channels of a unit of the others
 };
 struct Where {
     uint32_t bits;  // the unit of the row 0-7, head 8-18, token 19-25, kind 26-27
@@ -235,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) k_rotate(const __grid_constant__ Rot
         w[k] = where(i, nt, nh, per_token, kinds);
         const T* src = reinterpret_cast<const T*>(x.p) + (t0 + w[k].t()) * x.ts + (h0 + w[k].h()) * x.hs;
         if (w[k].kind() == 0) load_turn(v[k], src, w[k].u(), r);
-        else v[k].a = load8(src + other_channel(r, w[k].u()));
+        else load_plain(v[k], src + other_channel(r, w[k].u(), kinds.width), kinds.width);
     }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = divide(i, pairs), p = i - t * half;
@@ -248,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) k_rotate(const __grid_constant__ Rot
         if (i >= total) continue;
         T* dst = reinterpret_cast<T*>(y.p) + (t0 + w[k].t()) * y.ts + (h0 + w[k].h()) * y.hs;
         if (w[k].kind() == 0) store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
-        else store8(dst + other_channel(r, w[k].u()), v[k].a);
+        else store_plain(v[k], dst + other_channel(r, w[k].u(), kinds.width), kinds.width);
     }
 }
 
@@ -307,7 +332,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
         const HeadsView& x = w[k].kind() == 2 ? a.v : a.k;
         const In* src = reinterpret_cast<const In*>(x.p) + (int64_t)(t0 + w[k].t()) * x.ts + (h0 + w[k].h()) * x.hs;
         if (w[k].kind() == 0) load_turn(v[k], src, w[k].u(), r);
-        else v[k].a = load8(src + (w[k].kind() == 1 ? other_channel(r, w[k].u()) : 8 * w[k].u()));
+        else if (w[k].kind() == 1) load_plain(v[k], src + other_channel(r, w[k].u(), kinds.width), kinds.width);
+        else load_plain(v[k], src + 16 * w[k].u(), 16);
     }
     for (int i = threadIdx.x; i <= a.c.batch; i += kThreads) cu[i] = a.cu[i];
     __syncthreads();
@@ -344,13 +370,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
         const int64_t at = row[w[k].t()];
         if (at < 0) continue;
         Out* dst = reinterpret_cast<Out*>(w[k].kind() == 2 ? a.c.v : a.c.k) + at + (int64_t)(h0 + w[k].h()) * PAGE * dim;
-        if (w[k].kind() == 0) {
-            store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
-        } else {
-            Vec8<Out> o;
-            convert8(v[k].a, o);
-            store8(dst + (w[k].kind() == 1 ? other_channel(r, w[k].u()) : 8 * w[k].u()), o);
-        }
+        if (w[k].kind() == 0) store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
+        else if (w[k].kind() == 1) store_plain(v[k], dst + other_channel(r, w[k].u(), kinds.width), kinds.width);
+        else store_plain(v[k], dst + 16 * w[k].u(), 16);
     }
     if (a.start && blockIdx.x == 0 && blockIdx.y == 0) count_tokens(a, cu, threadIdx.x, kThreads);
 }
@@ -358,6 +380,12 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
 // The counts when they are also the start: after every CTA has read them.
 __global__ void k_kv_count(const __grid_constant__ KvAppend a) {
     count_tokens(a, a.cu, threadIdx.x, blockDim.x);
+}
+
+// Units of a row of dim channels, `others` of which are only moved, and of its values.
+Kinds kinds_of(const RotaryView& r, int others, int values) {
+    const int width = r.offset % 16 == 0 && others % 16 == 0 ? 16 : 8;
+    return {divisor(rot_units(r.rot, r.neighbours)), divisor(others / width), divisor(values / 16), width};
 }
 
 // Tokens and heads of a CTA: as many as its threads have units for, or fewer
@@ -377,7 +405,7 @@ template <typename T>
 cudaError_t rotate_as(const RotaryView& r, const HeadsView& x, const HeadsView& y, int64_t n_tokens, int heads, int dim,
                       cudaStream_t st) {
     const bool in_place = x.p == y.p;  // the other channels are there already
-    const Kinds kinds = {divisor(rot_units(r.rot, r.neighbours)), divisor(in_place ? 0 : (dim - r.rot) / 8), divisor(0)};
+    const Kinds kinds = kinds_of(r, in_place ? 0 : dim - r.rot, 0);
     const int units = kinds.turn.d + kinds.other.d;
     int tt, ht;
     tile_rows(n_tokens, heads, units, r.rot / 2, kUnits<T>, tt, ht);
@@ -390,7 +418,7 @@ cudaError_t rotate_as(const RotaryView& r, const HeadsView& x, const HeadsView& 
 template <typename In, typename Out>
 cudaError_t append_as(const KvAppend& a, const RotaryView& r, int dim, cudaStream_t st) {
     if (a.total > 0) {
-        const Kinds kinds = {divisor(rot_units(r.rot, r.neighbours)), divisor((dim - r.rot) / 8), divisor(dim / 8)};
+        const Kinds kinds = kinds_of(r, dim - r.rot, dim);
         int tt, ht;
         const int units = kinds.turn.d + kinds.other.d + kinds.value.d;
         tile_rows(a.total, a.c.kv_heads, units, r.rot / 2, kUnits<In>, tt, ht);
