@@ -40,25 +40,32 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf) {
     return r;
 }
 
+// x 2^e in two factors that are floats; never 0 for a positive x, so that a masked
+// score times it is -infinity.
+__device__ __forceinline__ float times_pow2(float x, int e) {
+    const int e1 = e / 2;
+    return fmaxf(x * pow2i(e1) * pow2i(e - e1), FLT_MIN);
+}
+
 // A 16-byte chunk of a row of bf16 queries, held by kChunks neighbouring lanes,
-// to fp16 times a power of two that takes the row's largest magnitude into
-// [2^14, 2^15).  Returns c (the softmax scale in log2 units) with the power undone.
+// to fp16 times 2^e, which takes the row's largest magnitude into [2^14, 2^15).
+// Returns e.
 template <int kChunks>
-__device__ __forceinline__ float scale_row(uint4& v, float c) {
+__device__ __forceinline__ int scale_row(uint4& v) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
 #pragma unroll
     for (int d = kChunks / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const int e = top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127);  // in two factors that are floats
-    const int e1 = e / 2, e2 = e - e1;
-    const float f1 = pow2i(e1), f2 = pow2i(e2);
+    const int e = top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127);
+    const int e1 = e / 2;
+    const float f1 = pow2i(e1), f2 = pow2i(e - e1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[i] = pack16(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2, false);
     v = make_uint4(w[0], w[1], w[2], w[3]);
-    return fmaxf(c * pow2i(-e1) * pow2i(-e2), FLT_MIN);  // never 0: a masked score is -infinity
+    return e;
 }
 
 // The items that a range's end divides: blockIdx.x the CTA that begins it,
@@ -158,7 +165,7 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaS
 // sequence: 16 or 32, or 0 when they are more (the chunk kernel's calls).
 inline int kv_rows_tile(int max_new, int g) {
     const int64_t rows = (int64_t)max_new * g;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+    return rows <= 16 ? 16 : 0;
 }
 
 }  // namespace csa2

@@ -52,32 +52,38 @@ constexpr int kTile = 256;  // rows of an item
 constexpr int kBlk = 128;   // keys of a block
 constexpr int kOver = 2;    // an item's start and end, in blocks
 constexpr int kWarpMma = 8, kWarpTma = 9;
-// The last warps load: two the queries of a 16-bit cache's call; the blocks of an
-// E4M3 cache are widened on the way, by seven.
-constexpr int load_warps(int mode) { return is_e4m3(mode) ? 7 : 2; }
+// The last warps load the queries: two, or six that widen an E4M3 cache's blocks too.
+constexpr int load_warps(int mode) { return is_e4m3(mode) ? 6 : 2; }
 constexpr int threads_of(int mode) { return is_e4m3(mode) ? 512 : 384; }
 // Registers of a thread at launch, of a softmax thread and of the others.
 constexpr int regs_launch(int mode) { return is_e4m3(mode) ? 128 : 168; }
 constexpr int regs_softmax(int mode) { return is_e4m3(mode) ? 168 : 208; }
 constexpr int regs_other(int) { return 88; }
 constexpr int kMixEvery = 4;  // of so many pairs of exponentials one is a polynomial
+constexpr int kExp = 113;   // scale_row's powers lie in [-113, 140]
 constexpr int kRing = 16;   // blocks whose masks of bad pages are kept
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // two of each, 128 columns apart
+// Laid at a multiple of 1,024 bytes.
 template <int kDim, int kMode>
-struct __align__(1024) Smem {
+struct Smem {
     static constexpr int kSlabs = kDim / 64;
-    static constexpr int kStages = kDim == 64 ? 8 : (is_e4m3(kMode) ? 4 : 5);
-    uint8_t q[2][kSlabs][128 * 128];            // [tile], slabs of 64 channels, SW128
-    uint8_t kv[kStages][kSlabs][kBlk * 128];    // K and V blocks by turns
-    float qc[is_e4m3(kMode) ? 2 : 1][is_e4m3(kMode) ? kTile : 4];  // c of each row (per item parity)
+    static constexpr int kStages = kDim == 64 ? (is_e4m3(kMode) ? 6 : 8) : (is_e4m3(kMode) ? 3 : 5);
+    static constexpr int kRaw = is_e4m3(kMode) ? (kDim == 64 ? 8 : 4) : 1;  // blocks of E4M3 codes in flight
+    alignas(16) uint8_t q[2][kSlabs][128 * 128];  // [tile], slabs of 64 channels, SW128
+    uint8_t kv[kStages][kSlabs][kBlk * 128];    // K and V blocks as the MMAs read them
+    uint8_t raw[kRaw][is_e4m3(kMode) ? kBlk * kDim : 16];
+    uint8_t qe[2][kMode == kE4m3Bf16 ? kTile : 8];  // power of two of each row, + kExp (per item parity)
     uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
     uint64_t full[kStages], empty[kStages];
+    uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_done[2];  // p_full: [tile][half of the keys]
     uint64_t tail;                              // the TMA of a V block that needs zeroing landed
     uint64_t drained;
     uint64_t frag_full[2], frag_empty[2];
+    uint64_t pair_full, pair_empty;
+    float2 pair[128];                           // tile 1's (maximum, sum) of an item of one tile
     KvFrag frag[2];                             // this item and the next (rows = 0: no more)
     uint32_t tmem_base;
     int abort;
@@ -125,6 +131,25 @@ struct Ring {
     }
 };
 
+// An item of at most 128 rows is one tile: the two tiles' places in TMEM then take
+// its blocks by turns, each with its own maximum and sums, joined at the item's
+// end.  (With one place the tensor core and the softmax warps wait for each
+// other: a block of 128 keys took 3,600 cycles, now 1,900.)
+__device__ __forceinline__ bool one_tile(const KvFrag& f) { return f.rows <= 128; }
+
+// What the x-th place in the ring holds, of an item's 2 nb: K and V by turns, or
+// for one tile K a block ahead (K0 K1 V0 K2 V1 ..), the order of their use.
+struct Part {
+    int j;
+    bool is_v;
+};
+__device__ __forceinline__ Part part_of(int x, int nb, bool one) {
+    if (!one) return {x >> 1, (x & 1) != 0};
+    if (x == 0) return {0, false};
+    if (x == 2 * nb - 1) return {nb - 1, true};
+    return x & 1 ? Part{(x + 1) >> 1, false} : Part{(x >> 1) - 1, true};
+}
+
 // ---------------------------------------------------------------- MMA
 
 template <int kDim, int kMode>
@@ -139,60 +164,72 @@ __device__ void role_mma(Smem<kDim, kMode>& sm, uint32_t tb) {
     const uint64_t desc_v = smem_desc(sm.kv[0][0], kBlk * 128, 1024, kLayoutSw128);
     Ring<S::kStages> ring;
     uint32_t items = 0, np[2] = {0, 0};  // items with keys; P hand-overs of each tile
-    auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
+    auto scores = [&](int t, int q, int stage) {  // S_t = Q_q K^T
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-            tc_mma_f16_w(tb + kColS + 128 * t, desc_q + off + ((t * S::kSlabs * 128 * 128) >> 4),
+            tc_mma_f16_w(tb + kColS + 128 * t, desc_q + off + ((q * S::kSlabs * 128 * 128) >> 4),
                          desc_k + off + ((stage * kStageBytes) >> 4), idesc_s, ks > 0);
         }
         tc_commit_w(&sm.s_full[t]);
     };
+    auto values = [&](int t, int stage, bool first) {  // O_t += P_t V, as P arrives
+        for (int half = 0; half < 2; ++half) {
+            if (!wait_bar_warp(sm, &sm.p_full[t][half], np[t] & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int i2 = 0; i2 < kBlk / 32; ++i2) {
+                const int i = i2 + half * (kBlk / 32);
+                tc_mma_f16_ta_w(tb + kColO + 128 * t, tb + kColS + 128 * t + 8 * i,
+                                desc_v + ((stage * kStageBytes + 2048 * i) >> 4), idesc_o, !first || i > 0);
+            }
+        }
+        ++np[t];
+        return true;
+    };
     for (uint32_t n = 0;; ++n) {
         if (!wait_bar_warp(sm, &sm.frag_full[n & 1], (n >> 1) & 1)) return;
-        const KvFrag& f = sm.frag[n & 1];
-        const int nb = f.f1 - f.f0, tiles = f.rows > 128 ? 2 : 1;
-        if (f.rows == 0) return;
+        const int nb = sm.frag[n & 1].f1 - sm.frag[n & 1].f0, rows = sm.frag[n & 1].rows;
+        const bool one = one_tile(sm.frag[n & 1]);
+        if (rows == 0) return;
         __syncwarp();
         mbar_arrive_w(&sm.frag_empty[n & 1]);
         if (nb == 0) continue;
         if (!wait_bar_warp(sm, &sm.q_full, items & 1)) return;
         ++items;
-        if (!wait_bar_warp(sm, &sm.full[ring.i], ring.phase)) return;
-        tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, ring.i);
-        tc_commit_w(&sm.empty[ring.i]);
-        if (nb == 1) tc_commit_w(&sm.q_empty);
-        ring.step();
+        // the first scores: of the first block for both tiles, or of the first two blocks
+        for (int t = 0; t < 2; ++t) {
+            if (one && t >= nb) break;
+            if (t == 0 || one) {
+                if (!wait_bar_warp(sm, &sm.full[ring.i], ring.phase)) return;
+                tc_fence_after();
+            }
+            scores(t, one ? 0 : t, ring.i);
+            if (t == 1 || one) {
+                tc_commit_w(&sm.empty[ring.i]);
+                ring.step();
+            }
+        }
+        if (nb == 1 || (one && nb == 2)) tc_commit_w(&sm.q_empty);
         for (int j = 0; j < nb; ++j) {
             const int sv = ring.i;
             const uint32_t pv = ring.phase;
             ring.step();
             const int sk = ring.i;
             const uint32_t pk = ring.phase;
-            const bool more = j + 1 < nb;
+            const bool more = j + (one ? 2 : 1) < nb;
             if (!wait_bar_warp(sm, &sm.full[sv], pv)) return;
             if (more && !wait_bar_warp(sm, &sm.full[sk], pk)) return;
-            for (int t = 0; t < tiles; ++t) {
-                for (int half = 0; half < 2; ++half) {  // O_t += P_t V, as P arrives
-                    if (!wait_bar_warp(sm, &sm.p_full[t][half], np[t] & 1)) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i2 = 0; i2 < kBlk / 32; ++i2) {
-                        const int i = i2 + half * (kBlk / 32);
-                        tc_mma_f16_ta_w(tb + kColO + 128 * t, tb + kColS + 128 * t + 8 * i,
-                                        desc_v + ((sv * kStageBytes + 2048 * i) >> 4), idesc_o, j > 0 || i > 0);
-                    }
-                }
-                ++np[t];
+            for (int t = one ? j & 1 : 0; t < (one ? (j & 1) + 1 : 2); ++t) {
+                if (!values(t, sv, j < (one ? 2 : 1))) return;
                 // in order behind the MMAs that read P, which S overwrites
-                if (more) scores(t, sk);
+                if (more) scores(t, one ? 0 : t, sk);
                 else tc_commit_w(&sm.o_done[t]);
             }
             tc_commit_w(&sm.empty[sv]);
             if (more) {
                 tc_commit_w(&sm.empty[sk]);
-                if (j + 2 == nb) tc_commit_w(&sm.q_empty);
+                if (j + (one ? 3 : 2) == nb) tc_commit_w(&sm.q_empty);
                 ring.step();
             }
         }
@@ -222,80 +259,93 @@ __device__ __forceinline__ PagePair pages_of(const KvAttn& a, const KvFrag& f, i
 }
 
 // A row of V that no query row of the item sees, or that is not loaded.
-__device__ __forceinline__ bool v_row_unseen(const KvFrag& f, const PagePair& pp, int j, int r) {
+__device__ __forceinline__ bool v_row_unseen(const KvFrag& f, int bad, int j, int r) {
     const int key = j * kBlk + r;
-    return key < f.v.lo || key > f.v.hi || pp.p[r >> 6] < 0;
+    return key < f.v.lo || key > f.v.hi || (bad >> (r >> 6) & 1);
 }
 
 template <int kDim, int kMode>
 __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor cur) {
     using S = Smem<kDim, kMode>;
+    constexpr bool kRawCodes = is_e4m3(kMode);
+    constexpr int kN = kRawCodes ? S::kRaw : S::kStages, kPageBytes = PAGE * kDim * (kRawCodes ? 1 : 2);
+    uint64_t* const fulls = kRawCodes ? sm.raw_full : sm.full;
+    uint64_t* const empties = kRawCodes ? sm.raw_empty : sm.empty;
     const int lane = threadIdx.x & 31;
-    Ring<S::kStages> ring;
+    Ring<kN> ring;
     uint32_t used = 0, tails = 0, blocks = 0;
     KvFrag f;
-    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {  // lanes 0 .. 2 kSlabs - 1, a box each
-        const int i = lane / S::kSlabs, c = lane % S::kSlabs;
-        if (lane < 2 * S::kSlabs && pp.p[i] >= 0)
-            tma_load_2d_nohint(&sm.kv[ring.i][c][i * PAGE * 128], is_v ? &maps.v : &maps.k, 64 * c,
-                               (pp.p[i] * a.c.kv_heads + h) * PAGE, bar);
+    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {
+        if constexpr (kRawCodes) {  // a page of a head is contiguous: a lane each
+            if (lane < 2 && pp.p[lane & 1] >= 0)
+                bulk_load_nohint(&sm.raw[ring.i][(lane & 1) * kPageBytes],
+                                 (is_v ? a.c.v : a.c.k) + ((int64_t)pp.p[lane & 1] * a.c.kv_heads + h) * kPageBytes, kPageBytes, bar);
+        } else {  // lanes 0 .. 2 kSlabs - 1, a box each
+            const int i = lane / S::kSlabs, c = lane % S::kSlabs;
+            if (lane < 2 * S::kSlabs && pp.p[i & 1] >= 0)
+                tma_load_2d_nohint(&sm.kv[ring.i][c][i * PAGE * 128], is_v ? &maps.v : &maps.k, 64 * c,
+                                   (pp.p[i & 1] * a.c.kv_heads + h) * PAGE, bar);
+        }
         __syncwarp();
     };
     bool alive = true;
     while (alive && cur.next(a, g, f)) {
         const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
-        int ids = -1;
-        for (int j = f.f0; j < f.f1 && alive; ++j, ++blocks) {
-            if (j == f.f0 || (2 * j & 31) == 0) {  // 32 page ids at a time, one to a lane
-                const int pg = (2 * j & ~31) + lane;
-                ids = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
+        const int nb = f.f1 - f.f0;
+        const bool one = one_tile(f);
+        int ids[2] = {-1, -1}, have[2] = {-1, -1};  // 32 page ids at a time, one to a lane: of K and of V
+        for (int x = 0; x < 2 * nb && alive; ++x) {
+            const Part part = part_of(x, nb, one);
+            const int j = f.f0 + part.j, is_v = part.is_v;
+            if (have[is_v] != 2 * j / 32) {
+                have[is_v] = 2 * j / 32;
+                const int pg = 32 * have[is_v] + lane;
+                ids[is_v] = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
             }
-            const PagePair pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids, 2 * j & 31),
-                                         __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31));
-            if (pp.bad && lane == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
-            const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * PAGE * kDim * 2;
-            const bool part = j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || pp.bad;
-            for (int is_v = 0; is_v < 2; ++is_v) {
-                if (used >= S::kStages && !(alive = wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1))) break;
-                ++used;
-                uint64_t* full = &sm.full[ring.i];
-                if (!is_v && lane == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
-                __syncwarp();
-                if (!is_v || !part) {
-                    mbar_expect_tx_w(full, bytes);
-                    load(pp, is_v, f.h, full);
-                } else {
-                    if (bytes) {
-                        mbar_expect_tx_w(&sm.tail, bytes);
-                        load(pp, true, f.h, &sm.tail);
-                        // its own copy: waited for even when the others have given up
-                        if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
-                            atomicExch(&sm.abort, 1);
-                            alive = false;
-                            break;
-                        }
-                        ++tails;
+            const PagePair pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids[is_v], 2 * j & 31),
+                                         __shfl_sync(0xffffffffu, ids[is_v], (2 * j + 1) & 31));
+            const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * kPageBytes;
+            if (used >= kN && !(alive = wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1))) break;
+            ++used;
+            uint64_t* full = &fulls[ring.i];
+            if (!is_v && lane == 0) {
+                sm.bad[(blocks + part.j) % kRing] = (uint8_t)pp.bad;
+                if (pp.bad) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+            }
+            __syncwarp();
+            if (kRawCodes || !is_v || (j * kBlk >= f.v.lo && j * kBlk + kBlk - 1 <= f.v.hi && !pp.bad)) {
+                mbar_expect_tx_w(full, bytes);
+                load(pp, is_v, f.h, full);
+            } else {
+                if (bytes) {
+                    mbar_expect_tx_w(&sm.tail, bytes);
+                    load(pp, true, f.h, &sm.tail);
+                    // its own copy: waited for even when the others have given up
+                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
+                        atomicExch(&sm.abort, 1);
+                        alive = false;
+                        break;
                     }
-                    for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
-                        const int r = (i >> 3) % kBlk;
-                        if (v_row_unseen(f, pp, j, r))
-                            *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    mbar_arrive_w(full);
+                    ++tails;
                 }
-                ring.step();
+                for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
+                    const int r = (i >> 3) % kBlk;
+                    if (v_row_unseen(f, pp.bad, j, r))
+                        *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                mbar_arrive_w(full);
             }
+            ring.step();
         }
+        blocks += nb;
     }
     // no copy is in flight when the CTA ends, also after a wait that gave up
     if (*reinterpret_cast<volatile int*>(&sm.abort)) {
-        for (uint32_t k = 0; k < min(used, (uint32_t)S::kStages); ++k) {
-            const int st = (ring.i + S::kStages - 1 - (int)k) % S::kStages;
-            const uint32_t ph = st < ring.i ? ring.phase : ring.phase ^ 1;
-            (void)mbar_wait(&sm.full[st], ph);
+        for (uint32_t k = 0; k < min(used, (uint32_t)kN); ++k) {
+            const int st = (ring.i + kN - 1 - (int)k) % kN;
+            (void)mbar_wait(&fulls[st], st < ring.i ? ring.phase : ring.phase ^ 1);
         }
     }
 }
@@ -313,6 +363,7 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
     constexpr int kLoaders = 32 * load_warps(kMode);
     const int tid = threadIdx.x - (threads_of(kMode) - kLoaders);
     Ring<S::kStages> ring;
+    Ring<S::kRaw> raw;
     uint32_t used = 0, items = 0, blocks = 0;
     const uint32_t inv_g = 65536u / g + 1;  // x / g = x * inv_g >> 16 for x < 256 + g
     KvFrag f;
@@ -343,7 +394,6 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
                 uint8_t* dst = &sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)];
                 if (r < f.rows) cp_async16(dst, q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
                 else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-                if (kMode == kE4m3F16 && c == 0) sm.qc[items & 1][r] = fmaxf(a.scale * kLog2e, FLT_MIN);
             }
             cp_async_commit();
             cp_async_wait_all();
@@ -361,9 +411,9 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = i0 + k * kLoaders, r = i / kChunks, c = i % kChunks;
-                    const float k2 = scale_row<kChunks>(v[k], fmaxf(a.scale * kLog2e, FLT_MIN));
+                    const int e = scale_row<kChunks>(v[k]);
                     if (r < rows) {
-                        if (c == 0) sm.qc[items & 1][r] = k2;
+                        if (c == 0) sm.qe[items & 1][r] = (uint8_t)(e + kExp);
                         *reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)]) = v[k];
                     }
                 }
@@ -374,68 +424,37 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         mbar_arrive_w(&sm.q_full);
         ++items;
         if constexpr (is_e4m3(kMode)) {
-            // ---- K and V: chunks of 16 channels, kLoaders apart; a block is taken in
-            // parts, each part's loads in flight while the part before is widened
-            constexpr int kCh = kDim / 16, kAll = kBlk * kCh, kPart = 3;
-            const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
-            const int last = f.v.hi / PAGE, first = f.v.lo / PAGE;
-            auto ids = [&](int j) {
-                return pages_of(a, f, j, 2 * j >= first && 2 * j <= last ? table[2 * j] : -1,
-                                2 * j + 1 >= first && 2 * j + 1 <= last ? table[2 * j + 1] : -1);
-            };
-            auto fetch = [&](const PagePair& pp, int j, bool is_v, int i0, uint4(&v)[kPart]) {
+            // ---- K and V: 16 codes to 32 bytes of fp16, four lanes to a row's 64 channels
+            // (the two rows of a quarter warp write all eight chunks of a line)
+            const int nb = f.f1 - f.f0;
+            const bool one = one_tile(f);
+            for (int x = 0; x < 2 * nb; ++x) {
+                const Part part = part_of(x, nb, one);
+                const int j = f.f0 + part.j;
+                if (!wait_bar_warp(sm, &sm.raw_full[raw.i], raw.phase)) return;
+                if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
+                ++used;
+                const int bad = sm.bad[(blocks + part.j) % kRing];
+                const bool zero = part.is_v && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
+                constexpr int kAll = kBlk * kDim / 16;
 #pragma unroll
-                for (int k = 0; k < kPart; ++k) {
-                    const int i = i0 + k * kLoaders, r = i / kCh, c16 = i % kCh, p = r < 64 ? pp.p[0] : pp.p[1];
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (i < kAll && p >= 0 && !(is_v && v_row_unseen(f, pp, j, r)))
-                        v[k] = *reinterpret_cast<const uint4*>(
-                            (is_v ? a.c.v : a.c.k) + (((int64_t)p * a.c.kv_heads + f.h) * PAGE + (r & 63)) * kDim + 16 * c16);
+                for (int i0 = 0; i0 < kAll; i0 += kLoaders) {
+                    const int i = i0 + tid, r = (i >> 2) % kBlk, slab = (i >> 2) / kBlk, c = i & 3;
+                    if (i >= kAll) break;
+                    uint4 v = *reinterpret_cast<const uint4*>(&sm.raw[raw.i][r * kDim + 64 * slab + 16 * c]), lo, hi;
+                    if (zero && v_row_unseen(f, bad, j, r)) v = make_uint4(0, 0, 0, 0);
+                    widen16(v, lo, hi);
+                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][slab][sw128(r, 2 * c)]) = lo;
+                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][slab][sw128(r, 2 * c + 1)]) = hi;
                 }
-            };
-            auto put = [&](int i0, const uint4(&v)[kPart]) {
-#pragma unroll
-                for (int k = 0; k < kPart; ++k) {
-                    const int i = i0 + k * kLoaders, r = i / kCh, c16 = i % kCh;
-                    if (i >= kAll) continue;
-                    uint4 lo, hi;
-                    widen16(v[k], lo, hi);
-                    uint8_t* slab = sm.kv[ring.i][c16 >> 2];
-                    const int ch = 2 * (c16 & 3);
-                    *reinterpret_cast<uint4*>(slab + sw128(r, ch)) = lo;
-                    *reinterpret_cast<uint4*>(slab + sw128(r, ch + 1)) = hi;
-                }
-            };
-            PagePair pp = ids(f.f0);
-            uint4 v[2][kPart];
-            constexpr int kParts = (kAll + kPart * kLoaders - 1) / (kPart * kLoaders);
-            fetch(pp, f.f0, false, tid, v[0]);
-#pragma unroll 1
-            for (int j = f.f0; j < f.f1; ++j, ++blocks) {
-                PagePair next = pp;
-                if (pp.bad && tid == 0) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
-                if (j + 1 < f.f1) next = ids(j + 1);
-#pragma unroll
-                for (int x = 0; x < 2 * kParts; ++x) {  // parts of K, then of V
-                    const bool is_v = x >= kParts;
-                    const int part = x % kParts, y = x + 1;
-                    if (y < 2 * kParts) fetch(pp, j, y >= kParts, tid + (y % kParts) * kPart * kLoaders, v[y & 1]);
-                    else if (j + 1 < f.f1) fetch(next, j + 1, false, tid, v[y & 1]);
-                    if (part == 0) {
-                        if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
-                        ++used;
-                        if (!is_v && tid == 0) sm.bad[blocks % kRing] = (uint8_t)pp.bad;
-                    }
-                    put(tid + part * kPart * kLoaders, v[x & 1]);
-                    if (part + 1 == kParts) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        mbar_arrive_w(&sm.full[ring.i]);
-                        ring.step();
-                    }
-                }
-                pp = next;
+                fence_proxy_async_smem();
+                __syncwarp();
+                mbar_arrive_w(&sm.full[ring.i]);
+                mbar_arrive_w(&sm.raw_empty[raw.i]);
+                ring.step();
+                raw.step();
             }
+            blocks += nb;
         }
     }
 }
@@ -492,7 +511,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
     const uint32_t ts = lane_base + kColS + 128 * t, to = lane_base + kColO + 128 * t;
     constexpr bool kP16Bf = kMode == kBf16;  // P in V's type
     constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
-    uint32_t ns = 0, no = 0, items = 0, blocks = 0;
+    uint32_t ns = 0, no = 0, items = 0, blocks = 0, pairs = 0;
     for (uint32_t n = 0;; ++n) {
         if (!wait_bar_warp(sm, &sm.frag_full[n & 1], (n >> 1) & 1)) return;
         const KvFrag& f = sm.frag[n & 1];
@@ -502,23 +521,25 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
         if (nb > 0) ++items;
         const int blk0 = blocks;
         blocks += nb;
-        if (f.rows > 128 * t) {
+        const bool one = one_tile(f);
+        if (!one || t == 0 || nb > 1) {
+            const int ri = one ? row : 128 * t + row;  // row of the item
             int pos, lo;  // the row sees keys lo .. pos
             {
-                const int x = min(f.tile * kTile - f.v.t0 * g + 128 * t + row, f.tile * kTile - f.v.t0 * g + f.rows - 1);
+                const int x = f.tile * kTile - f.v.t0 * g + min(ri, f.rows - 1);
                 pos = f.s.n - f.s.m + f.v.t0 + x / g;
                 lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
             }
             float mref = -INFINITY, l = 0.0f;
             float c = fmaxf(a.scale * kLog2e, FLT_MIN);  // never 0: a masked score is -infinity
-            const int j0 = f.f0, j1 = f.f1;
-            for (int j = j0; j < j1; ++j) {
+            const int j0 = f.f0, j1 = f.f1, first = one ? j0 + t : j0;
+            for (int j = first; j < j1; j += one ? 2 : 1) {
                 if (!wait_bar_warp(sm, &sm.s_full[t], ns & 1)) return;
                 ++ns;
                 __syncwarp();
                 tc_fence_after();
-                if constexpr (is_e4m3(kMode)) {
-                    if (j == j0) c = sm.qc[it & 1][128 * t + row];
+                if constexpr (kMode == kE4m3Bf16) {
+                    if (j == first) c = times_pow2(c, kExp - sm.qe[it & 1][ri]);
                 }
                 uint32_t r[4][32];
 #pragma unroll
@@ -543,7 +564,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                     const float f1 = move ? ex2(mref - bm) : 1.0f;  // mref = -inf: 0
                     if (move) mref = bm;
                     l *= f1;
-                    if (j > j0) {  // O holds the blocks before
+                    if (j > first) {  // O holds the blocks before
 #pragma unroll 1
                         for (int k = 0; k < kDim; k += 16) {
                             float o[16];
@@ -590,10 +611,32 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                 __syncwarp();
                 tc_fence_after();
             }
-            const bool mine = 128 * t + row < f.rows;
-            if (f.first && f.last) {
+            const bool both = one && nb > 1;  // tile 0 joins the two places' results
+            float w0 = 1.0f, w1 = 0.0f;
+            if (both && t == 1) {
+                sm.pair[row] = make_float2(mref, l);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_w(&sm.pair_full);
+                if (!wait_bar_warp(sm, &sm.pair_empty, pairs & 1)) return;
+            } else {
+                if (both) {
+                    if (!wait_bar_warp(sm, &sm.pair_full, pairs & 1)) return;
+                    __syncwarp();
+                    tc_fence_after();
+                    const float2 o = sm.pair[row];
+                    const float m = fmaxf(mref, o.x), ms = m == -INFINITY ? 0.0f : m;
+                    w0 = ex2(mref - ms), w1 = ex2(o.x - ms);  // a maximum of -infinity: 0
+                    l = l * w0 + o.y * w1;
+                    mref = m;
+                }
+                const bool mine = ri < f.rows;
+                const bool whole = f.first && f.last;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const int x = f.tile * kTile - f.v.t0 * g + min(128 * t + row, f.rows - 1);
+                const float k0 = whole ? w0 * inv : w0, k1 = whole ? w1 * inv : w1;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
+                float4* po = parts.o + slot * (kDim / 4) * kTile + ri;
+                const int x = f.tile * kTile - f.v.t0 * g + min(ri, f.rows - 1);
                 const int64_t token = f.s.row0 + f.v.t0 + x / g;
                 const int head = f.h * g + x % g;
                 uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
@@ -601,31 +644,43 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                 for (int k = 0; k < kDim; k += 32) {
                     float o[32];
                     if (nb > 0) tmem_ld_32x32b_x32(to + k, o);
+                    if (both) {
+                        float o1[32];
+                        tmem_ld_32x32b_x32(to + 128 + k, o1);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
+                        for (int i = 0; i < 32; ++i) o[i] = o[i] * k0 + o1[i] * k1;
+                    } else if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv, kOutBf);
-                        if (mine) *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 32; ++i) o[i] *= k0;
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    } else if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e], o[i + 2 * e + 1], kOutBf);
+                            *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
                 }
-                if (mine && a.lse) a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
-            } else {
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
-                float4* po = parts.o + slot * (kDim / 4) * kTile + 128 * t + row;
-#pragma unroll 1
-                for (int k = 0; k < kDim; k += 32) {
-                    float o[32];
-                    tmem_ld_32x32b_x32(to + k, o);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                if (!whole) {
+                    parts.ml[slot * kTile + ri] = make_float2(mref, l);
+                    if (f.first && threadIdx.x == 0)
+                        parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+                } else if (mine && a.lse) {
+                    a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
                 }
-                parts.ml[slot * kTile + 128 * t + row] = make_float2(mref, l);
-                if (f.first && threadIdx.x == 0)
-                    parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+                if (both) {
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_w(&sm.pair_empty);
+                }
             }
+            if (both) ++pairs;
             tc_fence_before();
         }
         __syncwarp();
@@ -657,6 +712,12 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
             mbar_init(&sm.frag_empty[t], 9);
             mbar_init(&sm.o_done[t], 1);
         }
+        for (int i = 0; i < S::kRaw; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], load_warps(kMode));
+        }
+        mbar_init(&sm.pair_full, 4);
+        mbar_init(&sm.pair_empty, 4);
         mbar_init(&sm.tail, 1);
         mbar_init(&sm.drained, 1);
         sm.abort = 0;
@@ -682,7 +743,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
     } else {
         regs_down<regs_other(kMode)>();
         if (warp == kWarpMma) role_mma<kDim, kMode>(sm, tb);
-        else if (warp == kWarpTma && !is_e4m3(kMode)) role_tma<kDim, kMode>(sm, a, maps, plan.g, cur);
+        else if (warp == kWarpTma) role_tma<kDim, kMode>(sm, a, maps, plan.g, cur);
         else role_load<kDim, kMode>(sm, a, plan.g, cur);
     }
     __syncwarp();
@@ -707,7 +768,7 @@ cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     static_assert(kSmem <= 232448, "shared memory beyond the 227 KB per-block limit");
     KvMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (!is_e4m3(kMode)) {
+    if (!is_e4m3(kMode)) {  // codes come by plain bulk copies
         const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
         if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode))
             return cudaErrorInvalidValue;

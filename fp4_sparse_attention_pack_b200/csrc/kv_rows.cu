@@ -189,8 +189,8 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                                                         (int64_t)(f.h * g + r - t * g) * a.q.hs + 8 * c);
                 }
                 if constexpr (kMode == kE4m3Bf16) {
-                    const float k = scale_row<kCh>(v, c0);
-                    if (c == 0) sm.qc[r] = k;
+                    const int e = scale_row<kCh>(v);
+                    if (c == 0) sm.qc[r] = times_pow2(c0, -e);
                 }
                 *reinterpret_cast<uint4*>(&sm.q[r][16 * c]) = v;
             }
