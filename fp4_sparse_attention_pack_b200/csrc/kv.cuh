@@ -42,9 +42,8 @@ __device__ __forceinline__ NewTokens new_tokens(const int32_t* cu, int b, int to
     return {a, e - a};
 }
 
-// Tokens that sequence b holds, clamped to the table's capacity.
-__device__ __forceinline__ int kv_held(const KvView& c, int b) {
-    int n = c.n_tokens[b];
+// Tokens that sequence b holds, clamped to the table's capacity; n: its count as stored.
+__device__ __forceinline__ int kv_held_of(const KvView& c, int n) {
     const int cap = c.max_pages * PAGE;
     if (n < 0 || n > cap) {
         atomicOr(c.status, CSA2_DEVERR_COUNT);
@@ -52,6 +51,7 @@ __device__ __forceinline__ int kv_held(const KvView& c, int b) {
     }
     return n;
 }
+__device__ __forceinline__ int kv_held(const KvView& c, int b) { return kv_held_of(c, c.n_tokens[b]); }
 
 // Physical page of a sequence's logical page, or -1 (and a status bit) when the
 // table points outside the pool.

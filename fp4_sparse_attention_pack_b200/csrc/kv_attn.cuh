@@ -47,71 +47,125 @@ __device__ __forceinline__ float times_pow2(float x, int e) {
     return fmaxf(x * pow2i(e1) * pow2i(e - e1), FLT_MIN);
 }
 
-// A 16-byte chunk of a row of bf16 queries, held by kChunks neighbouring lanes,
-// to fp16 times 2^e, which takes the row's largest magnitude into [2^14, 2^15).
-// Returns e.
-template <int kChunks>
-__device__ __forceinline__ int scale_row(uint4& v) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Queries in bf16 become fp16 times a power of two that takes the row's largest
+// magnitude into [2^14, 2^15): its exponent from the largest magnitude's bits, and
+// eight channels times it.
+__device__ __forceinline__ uint32_t top_bits(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-#pragma unroll
-    for (int d = kChunks / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const int e = top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127);
+    return top;
+}
+__device__ __forceinline__ int row_exp(uint32_t top) { return top == 0 ? 0 : 14 - ((int)max(top >> 7, 1u) - 127); }
+__device__ __forceinline__ uint4 scaled(const uint4& v, int e) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
     const int e1 = e / 2;
     const float f1 = pow2i(e1), f2 = pow2i(e - e1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[i] = pack16(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2, false);
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-    return e;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The items that a range's end divides: blockIdx.x the CTA that begins it,
-// blockIdx.y 32 of its rows (a warp's lanes); the warps share the channels.
-template <int kDim, bool kBf>
-__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttn a, const __grid_constant__ KvParts parts,
-                                                 int g, int tile_rows) {
+// The items that cuts divide.  A thread joins four channels of a row, four loads in
+// flight; when the items have many partial results each (few long sequences), 4 or
+// 16 threads take every 4th or 16th of them and meet in shared memory, in a fixed
+// order.  A task is `width` such columns of one item; the tasks of all items are spread over the blocks, which are as many
+// as run at once (a grid for each CTA that might be cut cost 4 us in waves of
+// blocks that have nothing to do).  kRowsFast: a partial result lies
+// [channels / 4][rows], else [rows][channels / 4].
+constexpr int kJoinThreads = 256, kJoinBlocksPerSm = 4;
+template <int kDim, bool kBf, bool kRowsFast>
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocksPerSm)
+    k_kv_join(const __grid_constant__ KvAttn a, const __grid_constant__ KvParts parts, int g, int tile_rows, int ctas) {
+    __shared__ float4 s_o[kJoinThreads];
+    __shared__ float2 s_ml[kJoinThreads];
+    __shared__ int s_cut[kJoinThreads], s_count[kJoinThreads / 32];
+    cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
-    const int cta = blockIdx.x;
-    const int4 cut = parts.cut[cta];
-    if (cut.w < 0) return;
-    const KvSeq s = kv_seq(a, cut.x);
-    const int row = 32 * blockIdx.y + (threadIdx.x & 31);
-    const int64_t r = (int64_t)cut.z * tile_rows + row;
-    if (r >= (int64_t)s.m * g) return;
-    float M = -INFINITY, L = 0.0f;
-    for (int k = cta; k <= cut.w; ++k) {
-        const float2 ml = parts.ml[(2 * (int64_t)k + (k == cta)) * tile_rows + row];
-        M = fmaxf(M, ml.x);
-    }
-    const float Ms = M == -INFINITY ? 0.0f : M;
-    float4 acc[kDim / 16];
-#pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = cta; k <= cut.w; ++k) {
-        const int64_t slot = 2 * (int64_t)k + (k == cta);
-        const float2 ml = parts.ml[slot * tile_rows + row];
-        const float w = exp2f(ml.x - Ms);
-        L += ml.y * w;
-#pragma unroll
-        for (int i = 0; i < kDim / 16; ++i) {
-            const float4 o = parts.o[(slot * (kDim / 4) + (threadIdx.x >> 5) + 4 * i) * tile_rows + row];
-            acc[i].x += w * o.x, acc[i].y += w * o.y, acc[i].z += w * o.z, acc[i].w += w * o.w;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = tile_rows * (kDim / 4);
+    for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {  // 256 CTAs' cuts at a time
+        const int c = c0 + threadIdx.x;
+        const bool is_cut = c < ctas && parts.cut[c].last >= 0;
+        const unsigned who = __ballot_sync(0xffffffffu, is_cut);
+        __syncthreads();
+        if (lane == 0) s_count[warp] = __popc(who);
+        __syncthreads();
+        int before = 0, cuts = 0;
+        for (int w = 0; w < kJoinThreads / 32; ++w) {
+            before += w < warp ? s_count[w] : 0;
+            cuts += s_count[w];
         }
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const int64_t token = s.row0 + r / g;
-    const int head = cut.y * g + (int)(r % g);
-    uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
+        if (is_cut) s_cut[before + __popc(who & ((1u << lane) - 1))] = c;
+        __syncthreads();
+        const int n = min(kJoinThreads, ctas - c0), groups = 16 * cuts < n ? 16 : 4 * cuts < n ? 4 : 1, width = kJoinThreads / groups;
+        const int tasks = cols / width, grp = threadIdx.x / width;
+        for (int task = blockIdx.x; task < cuts * tasks; task += gridDim.x) {
+            const int cta = s_cut[task / tasks], col = task % tasks * width + threadIdx.x % width;
+            const KvCut cut = parts.cut[cta];
+            const int row = kRowsFast ? col % tile_rows : col / (kDim / 4), chunk = kRowsFast ? col / tile_rows : col % (kDim / 4);
+            const int all = cut.last - cta + 1;
+            const bool mine = row < cut.rows;
+            float M = -INFINITY, L = 0.0f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kMany = 4;
+            for (int k0 = grp; mine && k0 < all; k0 += kMany * groups) {
+                float2 ml[kMany];
+                float4 o[kMany];
 #pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) {
-        uint2 w = make_uint2(pack16(acc[i].x * inv, acc[i].y * inv, kBf), pack16(acc[i].z * inv, acc[i].w * inv, kBf));
-        if (L == 0.0f) w = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(out + 4 * ((threadIdx.x >> 5) + 4 * i)) = w;
+                for (int i = 0; i < kMany; ++i) {
+                    const int k = k0 + i * groups;
+                    ml[i] = make_float2(-INFINITY, 0.0f);
+                    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < all) {
+                        const int64_t slot = 2 * (int64_t)(cta + k) + (k == 0);
+                        ml[i] = parts.ml[slot * tile_rows + row];
+                        o[i] = parts.o[slot * cols + col];
+                    }
+                }
+                float m = M;
+#pragma unroll
+                for (int i = 0; i < kMany; ++i) m = fmaxf(m, ml[i].x);
+                const float ms = m == -INFINITY ? 0.0f : m, w0 = exp2f(M - ms);
+                M = m;
+                L *= w0;
+                acc.x *= w0, acc.y *= w0, acc.z *= w0, acc.w *= w0;
+#pragma unroll
+                for (int i = 0; i < kMany; ++i) {
+                    const float w = exp2f(ml[i].x - ms);
+                    L += w * ml[i].y;
+                    acc.x += w * o[i].x, acc.y += w * o[i].y, acc.z += w * o[i].z, acc.w += w * o[i].w;
+                }
+            }
+            if (groups > 1) {
+                __syncthreads();  // the task before has been read
+                s_o[threadIdx.x] = acc;
+                s_ml[threadIdx.x] = make_float2(M, L);
+                __syncthreads();
+                if (grp > 0) continue;
+                for (int k = 1; k < min(groups, all); ++k) {
+                    const float2 ml = s_ml[k * width + threadIdx.x];
+                    const float4 o = s_o[k * width + threadIdx.x];
+                    const float m = fmaxf(M, ml.x), ms = m == -INFINITY ? 0.0f : m;
+                    const float w0 = exp2f(M - ms), w1 = exp2f(ml.x - ms);
+                    M = m;
+                    L = L * w0 + ml.y * w1;
+                    acc = make_float4(acc.x * w0 + o.x * w1, acc.y * w0 + o.y * w1, acc.z * w0 + o.z * w1, acc.w * w0 + o.w * w1);
+                }
+            }
+            if (!mine) continue;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            const int r = cut.row0 + row;
+            const int64_t token = cut.token0 + r / g;
+            const int head = cut.head0 + r % g;
+            uint2 w = make_uint2(pack16(acc.x * inv, acc.y * inv, kBf), pack16(acc.z * inv, acc.w * inv, kBf));
+            if (L == 0.0f) w = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs + 4 * chunk) = w;
+            if (a.lse && chunk == 0) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+        __syncthreads();  // s_cut has been read
     }
-    if (a.lse && threadIdx.x < 32) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 kv_encode_fn() {
@@ -144,12 +198,14 @@ inline bool make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int di
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch `kernel` so that its start overlaps the end of the launch before it.
+// Launch `kernel` so that its start overlaps the end of the launch before it
+// (it waits for that with cudaGridDependencySynchronize).
 template <typename... Args>
-cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

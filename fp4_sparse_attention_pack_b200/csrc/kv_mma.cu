@@ -51,6 +51,8 @@ using namespace sm100;
 constexpr int kTile = 256;  // rows of an item
 constexpr int kBlk = 128;   // keys of a block
 constexpr int kOver = 2;    // an item's start and end, in blocks
+constexpr int kMinPer = 4;  // least cost of a CTA's range
+constexpr int kSnap = 3;
 constexpr int kWarpMma = 8, kWarpTma = 9;
 // The last warps load the queries: two, or six that widen an E4M3 cache's blocks too.
 constexpr int load_warps(int mode) { return is_e4m3(mode) ? 6 : 2; }
@@ -387,36 +389,29 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) + (int64_t)(f.s.row0 + f.v.t0) * a.q.ts +
                             (int64_t)f.h * g * a.q.hs;
         const int rows = f.rows > 128 ? 256 : 128;
-        if constexpr (kMode != kE4m3Bf16) {
-            for (int i = tid; i < rows * kChunks; i += kLoaders) {
-                const int r = i / kChunks, c = i % kChunks;
-                const int x = rem0 + r, t = (x * inv_g) >> 16;
-                uint8_t* dst = &sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)];
-                if (r < f.rows) cp_async16(dst, q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
-                else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        for (int r = tid >> 1; r < rows; r += kLoaders / 2) {  // a pair of lanes to a row
+            const int x = rem0 + r, t = (x * inv_g) >> 16;
+            const uint16_t* src = q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * (tid & 1);
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint8_t* d = &sm.q[r >> 7][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))];
+                if (r < f.rows) cp_async16(d, src + 8 * c);
+                else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
             }
-            cp_async_commit();
-            cp_async_wait_all();
-        } else {
-            for (int i0 = tid; i0 < rows * kChunks; i0 += 4 * kLoaders) {  // rows * kChunks and kLoaders: whole warps
-                uint4 v[4];
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        if constexpr (kMode == kE4m3Bf16) {
+            for (int r = tid >> 1; r < rows; r += kLoaders / 2) {
+                auto at = [&](int c) { return reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))]); };
+                uint32_t top = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = i0 + k * kLoaders, r = i / kChunks, c = i % kChunks;
-                    const int x = rem0 + r, t = (x * inv_g) >> 16;
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (r < f.rows)
-                        v[k] = *reinterpret_cast<const uint4*>(q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * c);
-                }
+                for (int c = 0; c < kChunks; c += 2) top = max(top, top_bits(*at(c)));
+                top = max(top, __shfl_xor_sync(3u << (tid & 30), top, 1));
+                const int e = row_exp(top);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = i0 + k * kLoaders, r = i / kChunks, c = i % kChunks;
-                    const int e = scale_row<kChunks>(v[k]);
-                    if (r < rows) {
-                        if (c == 0) sm.qe[items & 1][r] = (uint8_t)(e + kExp);
-                        *reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, c & 7)]) = v[k];
-                    }
-                }
+                for (int c = 0; c < kChunks; c += 2) *at(c) = scaled(*at(c), e);
+                if ((tid & 1) == 0) sm.qe[items & 1][r] = (uint8_t)(e + kExp);
             }
         }
         fence_proxy_async_smem();
@@ -506,7 +501,7 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
 
 template <int kDim, int kMode>
 __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, uint32_t tb) {
-    const int t = threadIdx.x >> 7, row = threadIdx.x & 127;  // tile; row = TMEM lane
+    const int t = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;  // tile; row = TMEM lane
     const uint32_t lane_base = tb + ((uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16);
     const uint32_t ts = lane_base + kColS + 128 * t, to = lane_base + kColO + 128 * t;
     constexpr bool kP16Bf = kMode == kBf16;  // P in V's type
@@ -640,6 +635,11 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                 const int64_t token = f.s.row0 + f.v.t0 + x / g;
                 const int head = f.h * g + x % g;
                 uint16_t* out = reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs;
+                uint16_t* to_row[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    to_row[i] = reinterpret_cast<uint16_t*>(__shfl_sync(
+                        0xffffffffu, reinterpret_cast<unsigned long long>(mine ? out : nullptr), (lane & 28) + i));
 #pragma unroll 1
                 for (int k = 0; k < kDim; k += 32) {
                     float o[32];
@@ -657,20 +657,34 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    } else if (mine) {
+                    } else {
+                        // four lanes exchange their 16-byte chunks, so that a store takes 64
+                        // bytes of each of eight rows, not 16 of 32
+                        uint32_t w[4][4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = l == 0.0f ? 0u : pack16(o[2 * i], o[2 * i + 1], kOutBf);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = l == 0.0f ? 0u : pack16(o[i + 2 * e], o[i + 2 * e + 1], kOutBf);
-                            *reinterpret_cast<uint4*>(out + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int d = 1; d < 4; d *= 2)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i & d) continue;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t give = lane & d ? w[i][e] : w[i | d][e];
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                                    if (lane & d) w[i][e] = got;
+                                    else w[i | d][e] = got;
+                                }
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)  // chunk lane % 4 of the i-th of the four rows
+                            if (to_row[i]) *reinterpret_cast<uint4*>(to_row[i] + k + 8 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
                     }
                 }
                 if (!whole) {
                     parts.ml[slot * kTile + ri] = make_float2(mref, l);
                     if (f.first && threadIdx.x == 0)
-                        parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+                        parts.cut[blockIdx.x] = kv_cut<kSnap>(f, blockIdx.x, per, g, kTile);
                 } else if (mine && a.lse) {
                     a.lse[token * a.H + head] = l == 0.0f ? -INFINITY : (mref + log2f(l)) * kLn2;
                 }
@@ -722,11 +736,13 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         mbar_init(&sm.drained, 1);
         sm.abort = 0;
         fence_mbar_init();
-        parts.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
     }
     if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, kTmemCols);
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+    if (tid == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
-    Cursor cur = kv_plan<kTile, kBlk, kOver>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    Cursor cur = kv_plan<kTile, kBlk, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     tc_fence_before();
     __syncthreads();
@@ -776,16 +792,15 @@ cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     KvPlan plan;
     plan.g = a.H / a.c.kv_heads;
     plan.grid = device_sm_count();
-    plan.min_per = 4;
+    plan.min_per = kMinPer;
     const KvParts parts = kv_parts(a.ws, plan.grid, kTile, kDim);
     static std::atomic<uint64_t> attr_done{0};
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_mma<kDim, kMode>), kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    k_kv_mma<kDim, kMode><<<plan.grid, threads_of(kMode), kSmem, st>>>(a, maps, plan, parts);
-    e = cudaGetLastError();
+    e = launch_behind(k_kv_mma<kDim, kMode>, dim3(plan.grid), threads_of(kMode), kSmem, st, a, maps, plan, parts);
     if (e != cudaSuccess) return e;
     constexpr bool kBf = kMode == kBf16 || kMode == kE4m3Bf16;
-    return launch_behind(k_kv_join<kDim, kBf>, dim3(plan.grid, kTile / 32), 128, st, a, parts, plan.g, kTile);
+    return launch_behind(k_kv_join<kDim, kBf, true>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, kTile, plan.grid);
 }
 
 }  // namespace

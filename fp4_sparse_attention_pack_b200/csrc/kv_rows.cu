@@ -41,6 +41,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kOver = 3;       // an item's start and end, in pages
 constexpr int kMinPer = 6;     // least cost of a CTA's range
+constexpr int kSnap = 1;
 constexpr int kCtasPerSm = 2;
 
 template <int kDim, int kMode, int kMT>
@@ -189,8 +190,11 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                                                         (int64_t)(f.h * g + r - t * g) * a.q.hs + 8 * c);
                 }
                 if constexpr (kMode == kE4m3Bf16) {
-                    const int e = scale_row<kCh>(v);
-                    if (c == 0) sm.qc[r] = times_pow2(c0, -e);
+                    uint32_t top = top_bits(v);  // the row's chunks are neighbouring lanes'
+#pragma unroll
+                    for (int d = kCh / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    v = scaled(v, row_exp(top));
+                    if (c == 0) sm.qc[r] = times_pow2(c0, -row_exp(top));
                 }
                 *reinterpret_cast<uint4*>(&sm.q[r][16 * c]) = v;
             }
@@ -432,8 +436,7 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
         const bool whole = f.first && f.last;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
         for (int i = threadIdx.x; i < kRows * (kDim / 8); i += 32 * kWarps) {
-            // the output's chunks run along a row, the partial sums' along the rows
-            const int r = whole ? i / (kDim / 8) : i % kRows, c = whole ? i % (kDim / 8) : i / kRows;
+            const int r = i / (kDim / 8), c = i % (kDim / 8);
             float M = -INFINITY, L = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm.ml[k][r][0]);
@@ -458,14 +461,14 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                                           8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
                 if (a.lse && c == 0) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
             } else {
-                float4* po = parts.o + (slot * (kDim / 4) + 2 * c) * kRows + r;
+                float4* po = parts.o + (slot * kRows + r) * (kDim / 4) + 2 * c;
                 po[0] = make_float4(v[0], v[1], v[2], v[3]);
-                po[kRows] = make_float4(v[4], v[5], v[6], v[7]);
+                po[1] = make_float4(v[4], v[5], v[6], v[7]);
                 if (c == 0) parts.ml[slot * kRows + r] = make_float2(M, L);
             }
         }
         if (!whole && f.first && threadIdx.x == 0)
-            parts.cut[blockIdx.x] = make_int4(f.b, f.h, f.tile, blockIdx.x + (int)((f.rest + per - 1) / per));
+            parts.cut[blockIdx.x] = kv_cut<kSnap>(f, blockIdx.x, per, g, 16 * kMT);
         warps_sync();  // the buffers are free for the next item
     }
 }
@@ -485,10 +488,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         sm.abort = 0;
         fence_mbar_init();
-        parts.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
     }
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+    if (threadIdx.x == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
-    const Cursor<kMT> cur = kv_plan<16 * kMT, PAGE, kOver>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    const Cursor<kMT> cur = kv_plan<16 * kMT, PAGE, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     __syncthreads();
     if (threadIdx.x < 32 * kWarps) role_rows<kDim, kMode, kMT>(sm, a, parts, per, plan.g, cur);
@@ -517,11 +522,10 @@ cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
     static std::atomic<uint64_t> attr_done{0};
     cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_rows<kDim, kMode, kMT>), kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    k_kv_rows<kDim, kMode, kMT><<<plan.grid, kThreads, kSmem, st>>>(a, maps, plan, parts);
-    e = cudaGetLastError();
+    e = launch_behind(k_kv_rows<kDim, kMode, kMT>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
     if (e != cudaSuccess) return e;
     constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
-    return launch_behind(k_kv_join<kDim, kOutBf>, dim3(plan.grid, 1), 128, st, a, parts, plan.g, 16 * kMT);
+    return launch_behind(k_kv_join<kDim, kOutBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, 16 * kMT, plan.grid);
 }
 
 template <int kDim, int kMode>
