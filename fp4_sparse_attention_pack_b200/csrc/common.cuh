@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
     return out;
 }
 
+// Four E4M3 codes to two pairs of fp16.
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
 // Exact fp32 value of a non-negative E4M3 code (the scales are never negative).
 __device__ __forceinline__ float e4m3_decode_pos(uint32_t code) {
     const uint32_t e = (code >> 3) & 15u, m = code & 7u;

@@ -180,22 +180,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 kv_encode_fn() {
     return fn;
 }
 
-// A pool as rows of head_dim channels; boxes of 64 rows x 128 bytes (64 bytes
-// when a row is no longer), swizzled by their width.
-inline bool make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int dim, int mode) {
+// A pool as rows of head_dim channels; boxes of 64 rows x `width` bytes.
+inline bool make_pool_map(CUtensorMap* m, const void* base, int64_t rows, int dim, int mode, int width, CUtensorMapSwizzle swizzle) {
     auto fn = kv_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
-    const int elem = is_e4m3(mode) ? 1 : 2, width = dim * elem < 128 ? dim * elem : 128;
+    const int elem = is_e4m3(mode) ? 1 : 2;
     cuuint64_t strides[1] = {(cuuint64_t)dim * elem};
     cuuint32_t box[2] = {(cuuint32_t)(width / elem), PAGE};
     cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType type = is_e4m3(mode)  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : mode == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launch `kernel` so that its start overlaps the end of the launch before it

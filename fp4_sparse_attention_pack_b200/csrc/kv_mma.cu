@@ -74,7 +74,7 @@ struct Smem {
     static constexpr int kRaw = is_e4m3(kMode) ? (kDim == 64 ? 8 : 4) : 1;  // blocks of E4M3 codes in flight
     alignas(16) uint8_t q[2][kSlabs][128 * 128];  // [tile], slabs of 64 channels, SW128
     uint8_t kv[kStages][kSlabs][kBlk * 128];    // K and V blocks as the MMAs read them
-    uint8_t raw[kRaw][is_e4m3(kMode) ? kBlk * kDim : 16];
+    uint8_t raw[kRaw][is_e4m3(kMode) ? kBlk * kDim : 16];  // slabs of 64 channels [key][64]
     uint8_t qe[2][kMode == kE4m3Bf16 ? kTile : 8];  // power of two of each row, + kExp (per item parity)
     uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
     uint64_t full[kStages], empty[kStages];
@@ -277,17 +277,11 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
     Ring<kN> ring;
     uint32_t used = 0, tails = 0, blocks = 0;
     KvFrag f;
-    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {
-        if constexpr (kRawCodes) {  // a page of a head is contiguous: a lane each
-            if (lane < 2 && pp.p[lane & 1] >= 0)
-                bulk_load_nohint(&sm.raw[ring.i][(lane & 1) * kPageBytes],
-                                 (is_v ? a.c.v : a.c.k) + ((int64_t)pp.p[lane & 1] * a.c.kv_heads + h) * kPageBytes, kPageBytes, bar);
-        } else {  // lanes 0 .. 2 kSlabs - 1, a box each
-            const int i = lane / S::kSlabs, c = lane % S::kSlabs;
-            if (lane < 2 * S::kSlabs && pp.p[i & 1] >= 0)
-                tma_load_2d_nohint(&sm.kv[ring.i][c][i * PAGE * 128], is_v ? &maps.v : &maps.k, 64 * c,
-                                   (pp.p[i & 1] * a.c.kv_heads + h) * PAGE, bar);
-        }
+    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {  // lanes 0 .. 2 kSlabs - 1, a box each
+        const int i = lane / S::kSlabs, c = lane % S::kSlabs;
+        if (lane < 2 * S::kSlabs && pp.p[i & 1] >= 0)
+            tma_load_2d_nohint(kRawCodes ? &sm.raw[ring.i][(c * kBlk + i * PAGE) * 64] : &sm.kv[ring.i][c][i * PAGE * 128],
+                               is_v ? &maps.v : &maps.k, 64 * c, (pp.p[i & 1] * a.c.kv_heads + h) * PAGE, bar);
         __syncwarp();
     };
     bool alive = true;
@@ -352,10 +346,12 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
     }
 }
 
-// Two channels of E4M3 to fp16 pairs: 16 codes to 32 bytes.
+// 16 codes to 32 bytes of fp16.
 __device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
-    lo = make_uint4(e4m3x2_to_h2(v.x & 0xFFFF), e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y & 0xFFFF), e4m3x2_to_h2(v.y >> 16));
-    hi = make_uint4(e4m3x2_to_h2(v.z & 0xFFFF), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w & 0xFFFF), e4m3x2_to_h2(v.w >> 16));
+    e4m3x4_to_h2(v.x, lo.x, lo.y);
+    e4m3x4_to_h2(v.y, lo.z, lo.w);
+    e4m3x4_to_h2(v.z, hi.x, hi.y);
+    e4m3x4_to_h2(v.w, hi.z, hi.w);
 }
 
 // Queries (both modes) and, for E4M3, K and V: 128 threads.
@@ -364,8 +360,6 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
     using S = Smem<kDim, kMode>;
     constexpr int kLoaders = 32 * load_warps(kMode);
     const int tid = threadIdx.x - (threads_of(kMode) - kLoaders);
-    Ring<S::kStages> ring;
-    Ring<S::kRaw> raw;
     uint32_t used = 0, items = 0, blocks = 0;
     const uint32_t inv_g = 65536u / g + 1;  // x / g = x * inv_g >> 16 for x < 256 + g
     KvFrag f;
@@ -420,35 +414,41 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         ++items;
         if constexpr (is_e4m3(kMode)) {
             // ---- K and V: 16 codes to 32 bytes of fp16, four lanes to a row's 64 channels
-            // (the two rows of a quarter warp write all eight chunks of a line)
-            const int nb = f.f1 - f.f0;
+            // (the two rows of a quarter warp write all eight chunks of a line).  Two
+            // groups of warps take the blocks by turns: one waits while the other works.
+            const int nb = f.f1 - f.f0, group = tid / (kLoaders / 2), gt = tid % (kLoaders / 2);
             const bool one = one_tile(f);
-            for (int x = 0; x < 2 * nb; ++x) {
+            for (int x = group; x < 2 * nb; x += 2) {
                 const Part part = part_of(x, nb, one);
                 const int j = f.f0 + part.j;
-                if (!wait_bar_warp(sm, &sm.raw_full[raw.i], raw.phase)) return;
-                if (used >= S::kStages && !wait_bar_warp(sm, &sm.empty[ring.i], ring.phase ^ 1)) return;
-                ++used;
+                const uint32_t place = used + x;
+                const int ri = place % S::kStages, rw = place % S::kRaw;
+                if (!wait_bar_warp(sm, &sm.raw_full[rw], (place / S::kRaw) & 1)) return;
+                if (place >= S::kStages && !wait_bar_warp(sm, &sm.empty[ri], (place / S::kStages - 1) & 1)) return;
                 const int bad = sm.bad[(blocks + part.j) % kRing];
                 const bool zero = part.is_v && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
-                constexpr int kAll = kBlk * kDim / 16;
+                // a warp takes 8 rows of 64 channels at a time: 512 bytes of codes, 1,024 of fp16
+                constexpr int kAll = kBlk * kDim / 512, kWarps = kLoaders / 64;
+                const int lane = tid & 31, r8 = lane >> 2, w = gt >> 5;
+                const uint8_t* src = &sm.raw[rw][16 * lane];
+                uint8_t* lo_at = sm.kv[ri][0] + sw128(r8, 2 * (lane & 3));
+                uint8_t* hi_at = sm.kv[ri][0] + sw128(r8, 2 * (lane & 3) + 1);
 #pragma unroll
-                for (int i0 = 0; i0 < kAll; i0 += kLoaders) {
-                    const int i = i0 + tid, r = (i >> 2) % kBlk, slab = (i >> 2) / kBlk, c = i & 3;
-                    if (i >= kAll) break;
-                    uint4 v = *reinterpret_cast<const uint4*>(&sm.raw[raw.i][r * kDim + 64 * slab + 16 * c]), lo, hi;
-                    if (zero && v_row_unseen(f, bad, j, r)) v = make_uint4(0, 0, 0, 0);
+                for (int u0 = 0; u0 < kAll; u0 += kWarps) {
+                    const int u = u0 + w;
+                    if (u0 + kWarps > kAll && u >= kAll) continue;
+                    uint4 v = *reinterpret_cast<const uint4*>(src + 512 * u), lo, hi;
+                    if (zero && v_row_unseen(f, bad, j, (8 * u + r8) % kBlk)) v = make_uint4(0, 0, 0, 0);
                     widen16(v, lo, hi);
-                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][slab][sw128(r, 2 * c)]) = lo;
-                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][slab][sw128(r, 2 * c + 1)]) = hi;
+                    *reinterpret_cast<uint4*>(lo_at + 1024 * u) = lo;
+                    *reinterpret_cast<uint4*>(hi_at + 1024 * u) = hi;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                mbar_arrive_w(&sm.full[ring.i]);
-                mbar_arrive_w(&sm.raw_empty[raw.i]);
-                ring.step();
-                raw.step();
+                mbar_arrive_w(&sm.full[ri]);
+                mbar_arrive_w(&sm.raw_empty[rw]);
             }
+            used += 2 * nb;
             blocks += nb;
         }
     }
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&sm.full[i], is_e4m3(kMode) ? load_warps(kMode) : 1);
+            mbar_init(&sm.full[i], is_e4m3(kMode) ? load_warps(kMode) / 2 : 1);
             mbar_init(&sm.empty[i], 1);
         }
         mbar_init(&sm.q_full, load_warps(kMode));
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], load_warps(kMode));
+            mbar_init(&sm.raw_empty[i], load_warps(kMode) / 2);
         }
         mbar_init(&sm.pair_full, 4);
         mbar_init(&sm.pair_empty, 4);
@@ -784,11 +784,12 @@ cudaError_t mma_as(const KvAttn& a, cudaStream_t st) {
     static_assert(kSmem <= 232448, "shared memory beyond the 227 KB per-block limit");
     KvMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (!is_e4m3(kMode)) {  // codes come by plain bulk copies
-        const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
-        if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode))
-            return cudaErrorInvalidValue;
-    }
+    const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
+    constexpr int kWidth = is_e4m3(kMode) ? 64 : 128;  // bytes of 64 channels
+    constexpr CUtensorMapSwizzle kSwizzle = is_e4m3(kMode) ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode, kWidth, kSwizzle) ||
+        !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode, kWidth, kSwizzle))
+        return cudaErrorInvalidValue;
     KvPlan plan;
     plan.g = a.H / a.c.kv_heads;
     plan.grid = device_sm_count();

@@ -286,8 +286,11 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                                 uint32_t q2[4];
                                 if constexpr (kMT > 1) load_q(mt, ks + k2, q2);
                                 const uint32_t(&q)[4] = kMT == 1 ? qf[kMT == 1 ? ks + k2 : 0] : q2;
-                                mma16816<false>(s[mt][0], q, e4m3x2_to_h2(b[k2] & 0xFFFF), e4m3x2_to_h2(b[k2] >> 16));
-                                mma16816<false>(s[mt][1], q, e4m3x2_to_h2(b[2 + k2] & 0xFFFF), e4m3x2_to_h2(b[2 + k2] >> 16));
+                                uint32_t w[4];
+                                e4m3x4_to_h2(b[k2], w[0], w[1]);
+                                e4m3x4_to_h2(b[2 + k2], w[2], w[3]);
+                                mma16816<false>(s[mt][0], q, w[0], w[1]);
+                                mma16816<false>(s[mt][1], q, w[2], w[3]);
                             }
                     }
                 }
@@ -362,8 +365,9 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             // even channels: bytes 0, 2 (keys 2 c, 2 c + 1); odd ones: bytes 1, 3
-                            const uint32_t e0 = e4m3x2_to_h2(__byte_perm(b[2 * u], 0, 0x4420)), e1 = e4m3x2_to_h2(__byte_perm(b[2 * u + 1], 0, 0x4420));
-                            const uint32_t d0 = e4m3x2_to_h2(__byte_perm(b[2 * u], 0, 0x4431)), d1 = e4m3x2_to_h2(__byte_perm(b[2 * u + 1], 0, 0x4431));
+                            uint32_t e0, e1, d0, d1;
+                            e4m3x4_to_h2(__byte_perm(b[2 * u], 0, 0x3120), e0, d0);
+                            e4m3x4_to_h2(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, d1);
 #pragma unroll
                             for (int mt = 0; mt < kMT; ++mt) {
                                 mma16816<false>(o[mt][t + 2 * u], p[mt], e0, e1);
@@ -512,7 +516,9 @@ cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
     KvMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
-    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode) || !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode))
+    constexpr CUtensorMapSwizzle swizzle = S::kRowBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode, S::kRowBytes, swizzle) ||
+        !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode, S::kRowBytes, swizzle))
         return cudaErrorInvalidValue;
     KvPlan plan;
     plan.g = a.H / a.c.kv_heads;
