@@ -72,12 +72,14 @@ struct Smem {
     static constexpr int kSlabs = kDim / 64;
     static constexpr int kStages = kDim == 64 ? (is_e4m3(kMode) ? 6 : 8) : (is_e4m3(kMode) ? 3 : 5);
     static constexpr int kRaw = is_e4m3(kMode) ? (kDim == 64 ? 8 : 4) : 1;  // blocks of E4M3 codes in flight
-    alignas(16) uint8_t q[2][kSlabs][128 * 128];  // [tile], slabs of 64 channels, SW128
-    uint8_t kv[kStages][kSlabs][kBlk * 128];    // K and V blocks as the MMAs read them
+    // K and V blocks as the MMAs read them: slabs of 64 channels [key][64], SW128; then
+    // the queries of tile 1 and of tile 0 in the same form.  Where every item of a call
+    // is one tile, the ring has the place of tile 1's queries too.
+    alignas(16) uint8_t kv[kStages + 2][kSlabs][kBlk * 128];
     uint8_t raw[kRaw][is_e4m3(kMode) ? kBlk * kDim : 16];  // slabs of 64 channels [key][64]
     uint8_t qe[2][kMode == kE4m3Bf16 ? kTile : 8];  // power of two of each row, + kExp (per item parity)
     uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages + 1], empty[kStages + 1];
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_done[2];  // p_full: [tile][half of the keys]
@@ -123,15 +125,18 @@ __device__ __forceinline__ void regs_down() {
 
 using Cursor = KvCursor<kTile, kBlk, kOver>;
 
-// Stage counter of the K / V ring.
-template <int kStages>
+// Stage counter of a ring.
 struct Ring {
-    int i = 0;
+    int n, i = 0;
     uint32_t phase = 0;
+    __device__ __forceinline__ explicit Ring(int n) : n(n) {}
     __device__ __forceinline__ void step() {
-        if (++i == kStages) i = 0, phase ^= 1;
+        if (++i == n) i = 0, phase ^= 1;
     }
 };
+
+template <class S>
+__device__ __forceinline__ int stages_of(const KvAttn& a, int g) { return S::kStages + (a.max_new <= 128 / g ? 1 : 0); }
 
 // An item of at most 128 rows is one tile: the two tiles' places in TMEM then take
 // its blocks by turns, each with its own maximum and sums, joined at the item's
@@ -155,22 +160,22 @@ __device__ __forceinline__ Part part_of(int x, int nb, bool one) {
 // ---------------------------------------------------------------- MMA
 
 template <int kDim, int kMode>
-__device__ void role_mma(Smem<kDim, kMode>& sm, uint32_t tb) {
+__device__ void role_mma(Smem<kDim, kMode>& sm, int stages, uint32_t tb) {
     using S = Smem<kDim, kMode>;
     constexpr uint32_t kFmt = kMode == kBf16 ? 1 : 0;
     const uint32_t idesc_s = idesc_f16(128, kBlk, kFmt, 0, 0);
     const uint32_t idesc_o = idesc_f16(128, kDim, kFmt, 0, 1);
     constexpr uint32_t kStageBytes = S::kSlabs * kBlk * 128;
-    const uint64_t desc_q = smem_desc(sm.q[0][0], 16, 1024, kLayoutSw128);
+    const uint64_t desc_q = smem_desc(sm.kv[S::kStages + 1][0], 16, 1024, kLayoutSw128);
     const uint64_t desc_k = smem_desc(sm.kv[0][0], 16, 1024, kLayoutSw128);
     const uint64_t desc_v = smem_desc(sm.kv[0][0], kBlk * 128, 1024, kLayoutSw128);
-    Ring<S::kStages> ring;
+    Ring ring(stages);
     uint32_t items = 0, np[2] = {0, 0};  // items with keys; P hand-overs of each tile
     auto scores = [&](int t, int q, int stage) {  // S_t = Q_q K^T
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-            tc_mma_f16_w(tb + kColS + 128 * t, desc_q + off + ((q * S::kSlabs * 128 * 128) >> 4),
+            tc_mma_f16_w(tb + kColS + 128 * t, desc_q + off - ((q * kStageBytes) >> 4),
                          desc_k + off + ((stage * kStageBytes) >> 4), idesc_s, ks > 0);
         }
         tc_commit_w(&sm.s_full[t]);
@@ -221,14 +226,17 @@ __device__ void role_mma(Smem<kDim, kMode>& sm, uint32_t tb) {
             const uint32_t pk = ring.phase;
             const bool more = j + (one ? 2 : 1) < nb;
             if (!wait_bar_warp(sm, &sm.full[sv], pv)) return;
-            if (more && !wait_bar_warp(sm, &sm.full[sk], pk)) return;
             for (int t = one ? j & 1 : 0; t < (one ? (j & 1) + 1 : 2); ++t) {
                 if (!values(t, sv, j < (one ? 2 : 1))) return;
-                // in order behind the MMAs that read P, which S overwrites
-                if (more) scores(t, one ? 0 : t, sk);
-                else tc_commit_w(&sm.o_done[t]);
+                if (one || t == 1) tc_commit_w(&sm.empty[sv]);
+                if (!more) {
+                    tc_commit_w(&sm.o_done[t]);
+                    continue;
+                }
+                if (!wait_bar_warp(sm, &sm.full[sk], pk)) return;
+                tc_fence_after();
+                scores(t, one ? 0 : t, sk);  // in order behind the MMAs that read P, which S overwrites
             }
-            tc_commit_w(&sm.empty[sv]);
             if (more) {
                 tc_commit_w(&sm.empty[sk]);
                 if (j + (one ? 3 : 2) == nb) tc_commit_w(&sm.q_empty);
@@ -270,11 +278,12 @@ template <int kDim, int kMode>
 __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor cur) {
     using S = Smem<kDim, kMode>;
     constexpr bool kRawCodes = is_e4m3(kMode);
-    constexpr int kN = kRawCodes ? S::kRaw : S::kStages, kPageBytes = PAGE * kDim * (kRawCodes ? 1 : 2);
+    constexpr int kPageBytes = PAGE * kDim * (kRawCodes ? 1 : 2);
+    const int places = kRawCodes ? S::kRaw : stages_of<S>(a, g);
     uint64_t* const fulls = kRawCodes ? sm.raw_full : sm.full;
     uint64_t* const empties = kRawCodes ? sm.raw_empty : sm.empty;
     const int lane = threadIdx.x & 31;
-    Ring<kN> ring;
+    Ring ring(places);
     uint32_t used = 0, tails = 0, blocks = 0;
     KvFrag f;
     auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {  // lanes 0 .. 2 kSlabs - 1, a box each
@@ -301,7 +310,7 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
             const PagePair pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids[is_v], 2 * j & 31),
                                          __shfl_sync(0xffffffffu, ids[is_v], (2 * j + 1) & 31));
             const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * kPageBytes;
-            if (used >= kN && !(alive = wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1))) break;
+            if (used >= places && !(alive = wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1))) break;
             ++used;
             uint64_t* full = &fulls[ring.i];
             if (!is_v && lane == 0) {
@@ -339,8 +348,8 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
     }
     // no copy is in flight when the CTA ends, also after a wait that gave up
     if (*reinterpret_cast<volatile int*>(&sm.abort)) {
-        for (uint32_t k = 0; k < min(used, (uint32_t)kN); ++k) {
-            const int st = (ring.i + kN - 1 - (int)k) % kN;
+        for (uint32_t k = 0; k < min(used, (uint32_t)places); ++k) {
+            const int st = (ring.i + places - 1 - (int)k) % places;
             (void)mbar_wait(&fulls[st], st < ring.i ? ring.phase : ring.phase ^ 1);
         }
     }
@@ -388,7 +397,7 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
             const uint16_t* src = q + (int64_t)t * a.q.ts + (int64_t)(x - t * g) * a.q.hs + 8 * (tid & 1);
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
-                uint8_t* d = &sm.q[r >> 7][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))];
+                uint8_t* d = &sm.kv[S::kStages + 1 - (r >> 7)][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))];
                 if (r < f.rows) cp_async16(d, src + 8 * c);
                 else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
             }
@@ -397,7 +406,7 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         cp_async_wait_all();
         if constexpr (kMode == kE4m3Bf16) {
             for (int r = tid >> 1; r < rows; r += kLoaders / 2) {
-                auto at = [&](int c) { return reinterpret_cast<uint4*>(&sm.q[r >> 7][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))]); };
+                auto at = [&](int c) { return reinterpret_cast<uint4*>(&sm.kv[S::kStages + 1 - (r >> 7)][c >> 3][sw128(r & 127, (c & 7) + (tid & 1))]); };
                 uint32_t top = 0;
 #pragma unroll
                 for (int c = 0; c < kChunks; c += 2) top = max(top, top_bits(*at(c)));
@@ -416,15 +425,16 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
             // ---- K and V: 16 codes to 32 bytes of fp16, four lanes to a row's 64 channels
             // (the two rows of a quarter warp write all eight chunks of a line).  Two
             // groups of warps take the blocks by turns: one waits while the other works.
+            const uint32_t stages = stages_of<S>(a, g);
             const int nb = f.f1 - f.f0, group = tid / (kLoaders / 2), gt = tid % (kLoaders / 2);
             const bool one = one_tile(f);
             for (int x = group; x < 2 * nb; x += 2) {
                 const Part part = part_of(x, nb, one);
                 const int j = f.f0 + part.j;
                 const uint32_t place = used + x;
-                const int ri = place % S::kStages, rw = place % S::kRaw;
+                const int ri = place % stages, rw = place % S::kRaw;
                 if (!wait_bar_warp(sm, &sm.raw_full[rw], (place / S::kRaw) & 1)) return;
-                if (place >= S::kStages && !wait_bar_warp(sm, &sm.empty[ri], (place / S::kStages - 1) & 1)) return;
+                if (place >= stages && !wait_bar_warp(sm, &sm.empty[ri], (place / stages - 1) & 1)) return;
                 const int bad = sm.bad[(blocks + part.j) % kRing];
                 const bool zero = part.is_v && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
                 // a warp takes 8 rows of 64 channels at a time: 512 bytes of codes, 1,024 of fp16
@@ -519,6 +529,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
         const bool one = one_tile(f);
         if (!one || t == 0 || nb > 1) {
             const int ri = one ? row : 128 * t + row;  // row of the item
+            const bool idle = ri - lane >= f.rows;     // a warp without rows: what it leaves in P reaches no row that counts
             int pos, lo;  // the row sees keys lo .. pos
             {
                 const int x = f.tile * kTile - f.v.t0 * g + min(ri, f.rows - 1);
@@ -533,6 +544,11 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                 ++ns;
                 __syncwarp();
                 tc_fence_after();
+                if (idle) {
+                    mbar_arrive_w(&sm.p_full[t][0]);
+                    mbar_arrive_w(&sm.p_full[t][1]);
+                    continue;
+                }
                 if constexpr (kMode == kE4m3Bf16) {
                     if (j == first) c = times_pow2(c, kExp - sm.qe[it & 1][ri]);
                 }
@@ -654,6 +670,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                         for (int i = 0; i < 32; ++i) o[i] *= k0;
                     }
                     if (!whole) {
+                        if (idle) break;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             po[(int64_t)((k + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -712,7 +729,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
     static_assert(sizeof(KvPlanSmem) <= sizeof(sm.kv), "the plan's arrays lie in the ring");
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
+        for (int i = 0; i <= S::kStages; ++i) {
             mbar_init(&sm.full[i], is_e4m3(kMode) ? load_warps(kMode) / 2 : 1);
             mbar_init(&sm.empty[i], 1);
         }
@@ -758,7 +775,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         role_softmax<kDim, kMode>(sm, a, parts, per, plan.g, tb);
     } else {
         regs_down<regs_other(kMode)>();
-        if (warp == kWarpMma) role_mma<kDim, kMode>(sm, tb);
+        if (warp == kWarpMma) role_mma<kDim, kMode>(sm, stages_of<S>(a, plan.g), tb);
         else if (warp == kWarpTma) role_tma<kDim, kMode>(sm, a, maps, plan.g, cur);
         else role_load<kDim, kMode>(sm, a, plan.g, cur);
     }
