@@ -56,6 +56,7 @@ constexpr int kSnap = 3;
 constexpr int kWarpMma = 8, kWarpTma = 9;
 // The last warps load the queries: two, or six that widen an E4M3 cache's blocks too.
 constexpr int load_warps(int mode) { return is_e4m3(mode) ? 6 : 2; }
+constexpr int kGroupWarps = 3;  // of a group that widens a block
 constexpr int threads_of(int mode) { return is_e4m3(mode) ? 512 : 384; }
 // Registers of a thread at launch, of a softmax thread and of the others.
 constexpr int regs_launch(int mode) { return is_e4m3(mode) ? 128 : 168; }
@@ -86,7 +87,7 @@ struct Smem {
     uint64_t tail;                              // the TMA of a V block that needs zeroing landed
     uint64_t drained;
     uint64_t frag_full[2], frag_empty[2];
-    uint64_t pair_full, pair_empty;
+    uint64_t pair_full, pair_empty;             // the places' results of an item of one tile
     float2 pair[128];                           // tile 1's (maximum, sum) of an item of one tile
     KvFrag frag[2];                             // this item and the next (rows = 0: no more)
     uint32_t tmem_base;
@@ -286,63 +287,77 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
     Ring ring(places);
     uint32_t used = 0, tails = 0, blocks = 0;
     KvFrag f;
-    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {  // lanes 0 .. 2 kSlabs - 1, a box each
-        const int i = lane / S::kSlabs, c = lane % S::kSlabs;
-        if (lane < 2 * S::kSlabs && pp.p[i & 1] >= 0)
-            tma_load_2d_nohint(kRawCodes ? &sm.raw[ring.i][(c * kBlk + i * PAGE) * 64] : &sm.kv[ring.i][c][i * PAGE * 128],
-                               is_v ? &maps.v : &maps.k, 64 * c, (pp.p[i & 1] * a.c.kv_heads + h) * PAGE, bar);
-        __syncwarp();
+    // the whole warp issues each box (a lane for each box took 1,000 cycles a block, as
+    // the lanes' copies are issued one after another with their operands moved first)
+    auto load = [&](const PagePair& pp, bool is_v, int h, uint64_t* bar) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (pp.p[i] < 0) continue;
+            const int y = (pp.p[i] * a.c.kv_heads + h) * PAGE;
+#pragma unroll
+            for (int c = 0; c < S::kSlabs; ++c)
+                tma_load_2d_nohint_w(kRawCodes ? &sm.raw[ring.i][(c * kBlk + i * PAGE) * 64] : &sm.kv[ring.i][c][i * PAGE * 128],
+                                     is_v ? &maps.v : &maps.k, 64 * c, y, bar);
+        }
+    };
+    // block j's K or V to the next place of the ring
+    auto put = [&](const PagePair& pp, int j, int place, bool is_v) {
+        if (used >= places && !wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1)) return false;
+        ++used;
+        uint64_t* full = &fulls[ring.i];
+        const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * kPageBytes;
+        if (!is_v) {
+            if (lane == 0) {
+                sm.bad[place % kRing] = (uint8_t)pp.bad;
+                if (pp.bad) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+            }
+            __syncwarp();
+        }
+        if (kRawCodes || !is_v || (j * kBlk >= f.v.lo && j * kBlk + kBlk - 1 <= f.v.hi && !pp.bad)) {
+            mbar_expect_tx_w(full, bytes);
+            load(pp, is_v, f.h, full);
+        } else {
+            if (bytes) {
+                mbar_expect_tx_w(&sm.tail, bytes);
+                load(pp, true, f.h, &sm.tail);
+                // its own copy: waited for even when the others have given up
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
+                    atomicExch(&sm.abort, 1);
+                    return false;
+                }
+                ++tails;
+            }
+            for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
+                const int r = (i >> 3) % kBlk;
+                if (v_row_unseen(f, pp.bad, j, r))
+                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_w(full);
+        }
+        ring.step();
+        return true;
     };
     bool alive = true;
     while (alive && cur.next(a, g, f)) {
         const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
-        const int nb = f.f1 - f.f0;
-        const bool one = one_tile(f);
-        int ids[2] = {-1, -1}, have[2] = {-1, -1};  // 32 page ids at a time, one to a lane: of K and of V
-        for (int x = 0; x < 2 * nb && alive; ++x) {
-            const Part part = part_of(x, nb, one);
-            const int j = f.f0 + part.j, is_v = part.is_v;
-            if (have[is_v] != 2 * j / 32) {
-                have[is_v] = 2 * j / 32;
-                const int pg = 32 * have[is_v] + lane;
-                ids[is_v] = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
-            }
-            const PagePair pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids[is_v], 2 * j & 31),
-                                         __shfl_sync(0xffffffffu, ids[is_v], (2 * j + 1) & 31));
-            const uint32_t bytes = ((pp.p[0] >= 0) + (pp.p[1] >= 0)) * kPageBytes;
-            if (used >= places && !(alive = wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1))) break;
-            ++used;
-            uint64_t* full = &fulls[ring.i];
-            if (!is_v && lane == 0) {
-                sm.bad[(blocks + part.j) % kRing] = (uint8_t)pp.bad;
-                if (pp.bad) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
-            }
-            __syncwarp();
-            if (kRawCodes || !is_v || (j * kBlk >= f.v.lo && j * kBlk + kBlk - 1 <= f.v.hi && !pp.bad)) {
-                mbar_expect_tx_w(full, bytes);
-                load(pp, is_v, f.h, full);
-            } else {
-                if (bytes) {
-                    mbar_expect_tx_w(&sm.tail, bytes);
-                    load(pp, true, f.h, &sm.tail);
-                    // its own copy: waited for even when the others have given up
-                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
-                        atomicExch(&sm.abort, 1);
-                        alive = false;
-                        break;
-                    }
-                    ++tails;
+        const int nb = f.f1 - f.f0, ahead = one_tile(f) ? 1 : 0;
+        int ids = -1, have = -1;  // 32 page ids at a time, one to a lane
+        PagePair pp = {{-1, -1}, 0};
+        for (int x = -ahead; x < nb && alive; ++x) {  // K of block x + ahead, then V of block x
+            const PagePair before = pp;
+            if (x + ahead < nb) {
+                const int j = f.f0 + x + ahead;
+                if (have != 2 * j / 32) {
+                    have = 2 * j / 32;
+                    const int pg = 32 * have + lane;
+                    ids = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
                 }
-                for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
-                    const int r = (i >> 3) % kBlk;
-                    if (v_row_unseen(f, pp.bad, j, r))
-                        *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                mbar_arrive_w(full);
+                pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids, 2 * j & 31), __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31));
+                alive = put(pp, j, blocks + x + ahead, false);
             }
-            ring.step();
+            if (x >= 0 && alive) alive = put(ahead ? before : pp, f.f0 + x, 0, true);
         }
         blocks += nb;
     }
@@ -361,6 +376,26 @@ __device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
     e4m3x4_to_h2(v.y, lo.z, lo.w);
     e4m3x4_to_h2(v.z, hi.x, hi.y);
     e4m3x4_to_h2(v.w, hi.z, hi.w);
+}
+
+// A block of codes, slabs of 64 channels [key][64], to fp16 as the MMAs read it: a warp
+// takes 8 rows of a slab at a time, 512 bytes to 1,024, four lanes to a row (the two
+// rows of a quarter warp write all eight chunks of a line).
+template <int kDim, int kUnroll, class Seen>
+__device__ __forceinline__ void widen(const uint8_t* raw, uint8_t* kv, int thread, const Seen& seen) {
+    constexpr int kAll = kBlk * kDim / 512;
+    const int lane = thread & 31, r8 = lane >> 2;
+    const uint8_t* src = raw + 16 * lane;
+    uint8_t* lo_at = kv + sw128(r8, 2 * (lane & 3));
+    uint8_t* hi_at = kv + sw128(r8, 2 * (lane & 3) + 1);
+#pragma unroll kUnroll
+    for (int u = thread >> 5; u < kAll; u += kGroupWarps) {
+        uint4 v = *reinterpret_cast<const uint4*>(src + 512 * u), lo, hi;
+        if (!seen((8 * u + r8) % kBlk)) v = make_uint4(0, 0, 0, 0);
+        widen16(v, lo, hi);
+        *reinterpret_cast<uint4*>(lo_at + 1024 * u) = lo;
+        *reinterpret_cast<uint4*>(hi_at + 1024 * u) = hi;
+    }
 }
 
 // Queries (both modes) and, for E4M3, K and V: 128 threads.
@@ -422,37 +457,28 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
         mbar_arrive_w(&sm.q_full);
         ++items;
         if constexpr (is_e4m3(kMode)) {
-            // ---- K and V: 16 codes to 32 bytes of fp16, four lanes to a row's 64 channels
-            // (the two rows of a quarter warp write all eight chunks of a line).  Two
-            // groups of warps take the blocks by turns: one waits while the other works.
+            // ---- K and V: two groups of warps take the blocks by turns, so that one waits
+            // while the other works
             const uint32_t stages = stages_of<S>(a, g);
-            const int nb = f.f1 - f.f0, group = tid / (kLoaders / 2), gt = tid % (kLoaders / 2);
+            const int nb = f.f1 - f.f0, group = tid / (32 * kGroupWarps), gt = tid % (32 * kGroupWarps);
             const bool one = one_tile(f);
-            for (int x = group; x < 2 * nb; x += 2) {
+            constexpr int kGroups = kLoaders / (32 * kGroupWarps);
+            // a place's parity says which turn of the ring it is only within one turn
+            static_assert(kGroups <= S::kStages && kGroups <= S::kRaw, "more groups than places");
+            for (int x = (group + kGroups - used % kGroups) % kGroups; x < 2 * nb; x += kGroups) {  // places group, group + kGroups, ..
                 const Part part = part_of(x, nb, one);
                 const int j = f.f0 + part.j;
                 const uint32_t place = used + x;
                 const int ri = place % stages, rw = place % S::kRaw;
-                if (!wait_bar_warp(sm, &sm.raw_full[rw], (place / S::kRaw) & 1)) return;
                 if (place >= stages && !wait_bar_warp(sm, &sm.empty[ri], (place / stages - 1) & 1)) return;
+                if (!wait_bar_warp(sm, &sm.raw_full[rw], (place / S::kRaw) & 1)) return;
                 const int bad = sm.bad[(blocks + part.j) % kRing];
                 const bool zero = part.is_v && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
-                // a warp takes 8 rows of 64 channels at a time: 512 bytes of codes, 1,024 of fp16
-                constexpr int kAll = kBlk * kDim / 512, kWarps = kLoaders / 64;
-                const int lane = tid & 31, r8 = lane >> 2, w = gt >> 5;
-                const uint8_t* src = &sm.raw[rw][16 * lane];
-                uint8_t* lo_at = sm.kv[ri][0] + sw128(r8, 2 * (lane & 3));
-                uint8_t* hi_at = sm.kv[ri][0] + sw128(r8, 2 * (lane & 3) + 1);
-#pragma unroll
-                for (int u0 = 0; u0 < kAll; u0 += kWarps) {
-                    const int u = u0 + w;
-                    if (u0 + kWarps > kAll && u >= kAll) continue;
-                    uint4 v = *reinterpret_cast<const uint4*>(src + 512 * u), lo, hi;
-                    if (zero && v_row_unseen(f, bad, j, (8 * u + r8) % kBlk)) v = make_uint4(0, 0, 0, 0);
-                    widen16(v, lo, hi);
-                    *reinterpret_cast<uint4*>(lo_at + 1024 * u) = lo;
-                    *reinterpret_cast<uint4*>(hi_at + 1024 * u) = hi;
-                }
+                const auto seen = [&](int r) { return !zero || !v_row_unseen(f, bad, j, r); };
+                // Two tiles' softmax warps need the issue slots, so few loads are in flight
+                // then; for one tile widening is what bounds the kernel.
+                if (one) widen<kDim, 4>(sm.raw[rw], sm.kv[ri][0], gt, seen);
+                else widen<kDim, 2>(sm.raw[rw], sm.kv[ri][0], gt, seen);
                 fence_proxy_async_smem();
                 __syncwarp();
                 mbar_arrive_w(&sm.full[ri]);
@@ -730,7 +756,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i <= S::kStages; ++i) {
-            mbar_init(&sm.full[i], is_e4m3(kMode) ? load_warps(kMode) / 2 : 1);
+            mbar_init(&sm.full[i], is_e4m3(kMode) ? kGroupWarps : 1);
             mbar_init(&sm.empty[i], 1);
         }
         mbar_init(&sm.q_full, load_warps(kMode));
@@ -745,7 +771,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], load_warps(kMode) / 2);
+            mbar_init(&sm.raw_empty[i], kGroupWarps);
         }
         mbar_init(&sm.pair_full, 4);
         mbar_init(&sm.pair_empty, 4);

@@ -144,10 +144,13 @@ __device__ void role_load(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvM
             }
             __syncwarp();
             mbar_expect_tx_w(&sm.full[st], good ? 2 * S::kPageBytes : 0);
-            if (good && lane < 2 * S::kSlabs) {
-                const int v = lane / S::kSlabs, c = lane % S::kSlabs;
-                tma_load_2d_nohint(&sm.kv[st][v][c * PAGE * S::kRowBytes], v ? &maps.v : &maps.k,
-                                   c * (S::kRowBytes / S::kElem), (id * a.c.kv_heads + f.h) * PAGE, &sm.full[st]);
+            if (good) {  // the whole warp issues each box
+#pragma unroll
+                for (int i = 0; i < 2 * S::kSlabs; ++i) {
+                    const int v = i / S::kSlabs, c = i % S::kSlabs;
+                    tma_load_2d_nohint_w(&sm.kv[st][v][c * PAGE * S::kRowBytes], v ? &maps.v : &maps.k,
+                                         c * (S::kRowBytes / S::kElem), (id * a.c.kv_heads + f.h) * PAGE, &sm.full[st]);
+                }
             }
             __syncwarp();
             if (++st == S::kStages) st = 0, phase ^= 1;
