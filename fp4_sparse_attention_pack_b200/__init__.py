@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from ._build import LIB
+from ._build import BIND, LIB
 
 __all__ = ["Csa2Error", "lib", "csa2_cache", "csa2_window", "csa2_model", "csa2_step_in",
            "csa2_step_out", "pack_cache", "index_topk", "index_topk_workspace", "index_pool_workspace",
@@ -265,32 +265,26 @@ def index_topk_noalloc(cache: csa2_cache, q_idx, w, K: int, idx_out, score_out=N
 
 # ---------------------------------------------------------------- paged key/value cache
 #
-# A decode step makes these calls with a few microseconds of device work each, so
-# their checks compare attributes only and the device guard is taken when needed.
+# The calls themselves (checks of the tensors, device guard, stream) are csrc/bind.cpp's.
 
-class _Names:
-    """torch's objects that every call compares with, looked up once."""
-
-    def __init__(self):
-        import torch
-        self.int32, self.float32 = torch.int32, torch.float32
-        self.heads = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
-        self.pools = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.float8_e4m3fn: KV_E4M3}
-        self.device = torch.cuda.device
-        self.current_device = torch.cuda.current_device
-        # the current stream's handle without a Stream object
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_bind = None
 
 
-_n = None
-
-
-def _names():
-    global _n
-    if _n is None:
-        _n = _Names()
-    return _n
+def _calls():
+    """The loaded module with the calls (raises if it is missing)."""
+    global _bind
+    if _bind is None:
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are loaded first)
+        if not os.path.exists(BIND):
+            raise ImportError(f"{BIND} is not built; run __graft_entry__.build() first")
+        spec = importlib.util.spec_from_file_location("_bind", BIND)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.init(*[ctypes.cast(f, _vp).value for f in (L.csa2_rotate, L.csa2_kv_append, L.csa2_kv_attn)])
+        _bind = m
+    return _bind
 
 
 def _want(t, what, dtype, shape, index=None):
@@ -304,48 +298,12 @@ def _want(t, what, dtype, shape, index=None):
     return at
 
 
-def _heads(t, what, shape, dtype, index):
-    """csa2_heads of a [tokens][heads][channels] tensor with contiguous channels."""
-    if t.get_device() != index or index < 0 or t.dtype is not dtype:
-        raise ValueError(f"{what} is {t.dtype} on {t.device}: it must be {dtype}, on the call's CUDA device")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    ts, hs, cs = t.stride()
-    if cs != 1 and shape[2] > 1:
-        raise ValueError(f"{what}: the channels must be contiguous")
-    return csa2_heads(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
-
-
-def _code(codes, t, what):
-    code = codes.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{what}: {t.dtype} is not supported")
-    return code
-
-
-def _on_cache(cache, index, what):
-    at = getattr(cache, "_index", index)
-    if at != index:
-        raise ValueError(f"{what} is on CUDA device {index}, the cache on {at}")
-
-
-def _call(f, index, stream, args, what):
-    """f(*args, stream) with tensor device `index` current."""
-    n = _names()
-    if n.current_device() == index:
-        rc = f(*args, n.stream(index) if stream is None else stream.cuda_stream)
-    else:
-        with n.device(index):
-            rc = f(*args, n.stream(index) if stream is None else stream.cuda_stream)
-    if rc != 0:
-        raise Csa2Error(rc, what)
-
-
 def rotary(inv_freq, rot_dim: int, offset: int = 0, neighbours: bool = False, n_axes: int = 1, axis=None) -> csa2_rotary:
     """A rotation: channels offset .. offset + rot_dim - 1 of a head turn in pairs (neighbours, or half the
     rotation apart) by position * inv_freq[pair] (fp32 CUDA tensor).  axis (a list, one entry per pair) says
     which of the n_axes positions turns it."""
-    index = _want(inv_freq, "inv_freq", _names().float32, (rot_dim // 2,))
+    import torch
+    index = _want(inv_freq, "inv_freq", torch.float32, (rot_dim // 2,))
     r = csa2_rotary(inv_freq.data_ptr(), None, rot_dim, offset, int(neighbours), n_axes)
     if axis is not None:
         if len(axis) != rot_dim // 2:
@@ -357,34 +315,30 @@ def rotary(inv_freq, rot_dim: int, offset: int = 0, neighbours: bool = False, n_
 
 def rotate(rot: csa2_rotary, x, pos, out, inverse: bool = False, stream=None):
     """out = x [tokens][heads][channels] rotated at pos int32 [n_axes][tokens] (out may be x); inverse turns back."""
-    n, index, shape = _names(), x.get_device(), x.shape
-    if len(shape) != 3:
-        raise ValueError(f"x must be [tokens][heads][channels], not {tuple(shape)}")
-    xd = _heads(x, "x", shape, x.dtype, index)
-    yd = _heads(out, "out", shape, x.dtype, index)
-    _want(pos, "pos", n.int32, (rot.n_axes, shape[0]), index)
-    _on_cache(rot, index, "x")
-    _call(lib().csa2_rotate, index, stream,
-          (ctypes.byref(rot), ctypes.byref(xd), ctypes.byref(yd), _code(n.heads, x, "x"), shape[0], shape[1], shape[2],
-           pos.data_ptr(), int(inverse)), "csa2_rotate")
+    rc = (_bind or _calls()).rotate(rot, x, pos, out, inverse, stream)
+    if rc:
+        raise Csa2Error(rc, "csa2_rotate")
 
 
 def kv_cache(k_pages, v_pages, page_table, n_tokens, status) -> csa2_kv_cache:
     """Descriptor of a paged key/value cache: pools [pages][kv_heads][64][head_dim] (bf16, fp16 or float8_e4m3fn),
     page_table int32 [batch][max_pages], n_tokens int32 [batch], status int32 (one word or more)."""
-    n = _names()
+    import torch
+    types = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.float8_e4m3fn: KV_E4M3}
     pages, heads, rows, dim = k_pages.shape
     if rows != 64:
         raise ValueError(f"a page has 64 rows, not {rows}")
+    if k_pages.dtype not in types:
+        raise ValueError(f"k_pages: {k_pages.dtype} is not supported")
     index = _want(k_pages, "k_pages", k_pages.dtype, k_pages.shape)
     _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape, index)
     batch, max_pages = page_table.shape
-    _want(page_table, "page_table", n.int32, (batch, max_pages), index)
-    _want(n_tokens, "n_tokens", n.int32, (batch,), index)
+    _want(page_table, "page_table", torch.int32, (batch, max_pages), index)
+    _want(n_tokens, "n_tokens", torch.int32, (batch,), index)
     if status.get_device() != index or status.element_size() != 4 or status.numel() < 1:
         raise ValueError("status must be a tensor of 32-bit words on the cache's device")
     c = csa2_kv_cache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), n_tokens.data_ptr(),
-                      status.data_ptr(), batch, max_pages, pages, heads, dim, _code(n.pools, k_pages, "k_pages"))
+                      status.data_ptr(), batch, max_pages, pages, heads, dim, types[k_pages.dtype])
     c._keep, c._index = (k_pages, v_pages, page_table, n_tokens, status), index  # the descriptor holds their addresses
     return c
 
@@ -393,20 +347,9 @@ def kv_append(cache: csa2_kv_cache, k, v, cu, max_new: int, start=None, rotary=N
     """Write the new tokens k, v [total][kv_heads][head_dim] (sequence b: rows cu[b] .. cu[b + 1] - 1) behind
     start (int32 [batch]; None: behind the tokens held), the keys rotated at pos int32 [n_axes][total]
     (None: their slots)."""
-    n, index, total, batch = _names(), k.get_device(), k.shape[0], cache.batch
-    shape = (total, cache.kv_heads, cache.head_dim)
-    kd, vd = _heads(k, "k", shape, k.dtype, index), _heads(v, "v", shape, k.dtype, index)
-    _on_cache(cache, index, "k")
-    _want(cu, "cu", n.int32, (batch + 1,), index)
-    if start is not None:
-        _want(start, "start", n.int32, (batch,), index)
-    if rotary is not None:
-        _on_cache(rotary, index, "k")
-    if pos is not None:
-        _want(pos, "pos", n.int32, (rotary.n_axes if rotary is not None else 0, total), index)
-    _call(lib().csa2_kv_append, index, stream,
-          (ctypes.byref(cache), ctypes.byref(kd), ctypes.byref(vd), _code(n.heads, k, "k"), cu.data_ptr(), total, max_new,
-           _ptr(start), ctypes.byref(rotary) if rotary is not None else None, _ptr(pos)), "csa2_kv_append")
+    rc = (_bind or _calls()).kv_append(cache, k, v, cu, max_new, start, rotary, pos, stream)
+    if rc:
+        raise Csa2Error(rc, "csa2_kv_append")
 
 
 def kv_attn_workspace(cache: csa2_kv_cache, total: int, max_new: int, H: int) -> int:
@@ -416,16 +359,6 @@ def kv_attn_workspace(cache: csa2_kv_cache, total: int, max_new: int, H: int) ->
 def kv_attn(cache: csa2_kv_cache, q, cu, max_new: int, scale: float, out, ws, lse=None, window: int = 0, stream=None):
     """out [total][H][head_dim] = attention of the new tokens' queries q over the cache (their own keys appended
     before); lse fp32 [total][H] (optional); window > 0: each token sees its last `window` keys only."""
-    n, index = _names(), q.get_device()
-    shape = (q.shape[0], q.shape[1], cache.head_dim)
-    qd, od = _heads(q, "q", shape, q.dtype, index), _heads(out, "out", shape, q.dtype, index)
-    _on_cache(cache, index, "q")
-    _want(cu, "cu", n.int32, (cache.batch + 1,), index)
-    if lse is not None:
-        _want(lse, "lse", n.float32, shape[:2], index)
-    if ws is not None and ws.get_device() != index:
-        raise ValueError(f"ws is on {ws.device}, not on the call's CUDA device")
-    _call(lib().csa2_kv_attn, index, stream,
-          (ctypes.byref(cache), ctypes.byref(qd), shape[1], _code(n.heads, q, "q"), cu.data_ptr(), shape[0], max_new, scale,
-           window, ctypes.byref(od), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0),
-          "csa2_kv_attn")
+    rc = (_bind or _calls()).kv_attn(cache, q, cu, max_new, scale, out, ws, lse, window, stream)
+    if rc:
+        raise Csa2Error(rc, "csa2_kv_attn")

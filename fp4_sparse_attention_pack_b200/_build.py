@@ -1,4 +1,5 @@
-"""In-tree build of the CUDA library (libcsa2.so) for sm_100a with nvcc."""
+"""In-tree build of the CUDA library (libcsa2.so) for sm_100a with nvcc, and of the module with the Python
+calls of the paged key/value operators (_bind.so) with g++ against torch's headers."""
 from __future__ import annotations
 
 import glob
@@ -10,6 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcsa2.so")
+BIND = os.path.join(PKG, "_bind.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -27,7 +29,25 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_bind(force: bool) -> None:
+    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "csa2.h")
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    libs = os.path.join(home, "lib")
+    dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(home, "include"),
+            os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                           *[f"-I{d}" for d in dirs], src, "-o", BIND, f"-L{libs}", f"-Wl,-rpath,{libs}",
+                           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_bind(force)
     if force or _stale():
         cmd = ["nvcc", *ARCH, *FLAGS, *sources(), "-o", LIB]
         if verbose:
