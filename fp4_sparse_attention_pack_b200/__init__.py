@@ -353,7 +353,10 @@ def kv_append(cache: csa2_kv_cache, k, v, cu, max_new: int, start=None, rotary=N
 
 
 def kv_attn_workspace(cache: csa2_kv_cache, total: int, max_new: int, H: int) -> int:
-    return int(lib().csa2_kv_attn_workspace(ctypes.byref(cache), total, max_new, H))
+    """Bytes of workspace for kv_attn calls of these sizes; what does for max_new does for fewer."""
+    import torch
+    with torch.cuda.device(getattr(cache, "_index", -1)):
+        return int(lib().csa2_kv_attn_workspace(ctypes.byref(cache), total, max_new, H))
 
 
 def kv_attn(cache: csa2_kv_cache, q, cu, max_new: int, scale: float, out, ws, lse=None, window: int = 0, stream=None):

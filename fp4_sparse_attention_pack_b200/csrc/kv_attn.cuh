@@ -215,11 +215,10 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_
 
 }  // namespace
 
-// Rows to an item of the few-rows kernel for calls of at most max_new tokens a
-// sequence: 16 or 32, or 0 when they are more (the chunk kernel's calls).
-inline int kv_rows_tile(int max_new, int g) {
-    const int64_t rows = (int64_t)max_new * g;
-    return rows <= 16 ? 16 : 0;
-}
+// Calls of at most 16 rows to an item go to the few-rows kernel.  (One token of 8
+// sequences over 32,768, 64 / 8 heads of 128: 177 us there, 199 us in the chunk
+// kernel; over an E4M3 cache of 65,536 229 and 339 us.  Two tiles of 16 rows in it,
+// 4 tokens each: 348 us against 192 us in the chunk kernel.)
+inline bool kv_few_rows(int max_new, int g) { return (int64_t)max_new * g <= 16; }
 
 }  // namespace csa2

@@ -495,8 +495,7 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
 // 2^t of two values in fp32 arithmetic, for t in [-126, 2^22): t = n + f with
 // |f| <= 1/2, a polynomial for 2^f (the minimax one of degree 4, computed for
 // this file by Remez exchange: relative error 2.6e-6, far below the rounding to
-// 16 bits) and n added to the exponent.  Below -126 the value is that of -126;
-// NaN gives a huge value, so that the row's result is not finite.
+// 16 bits) times 2^n.  Below -126 the value is that of -126; NaN stays NaN.
 __device__ __forceinline__ float2 ex2_poly(float2 t) {
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(-126.0f));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(-126.0f));
@@ -507,8 +506,8 @@ __device__ __forceinline__ float2 ex2_poly(float2 t) {
     p = fma2(p, f, splat2(0.2402474483f));
     p = fma2(p, f, splat2(0.6931218147f));
     p = fma2(p, f, splat2(0.9999992614f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(r.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(r.y) << 23)));
+    return mul2(p, make_float2(__uint_as_float((__float_as_uint(r.x) << 23) + 0x3F800000u),
+                               __uint_as_float((__float_as_uint(r.y) << 23) + 0x3F800000u)));
 }
 
 // P of 32 keys, 2^(c s - m), in 16 bits, and its sums.  kMix: some pairs by

@@ -1,5 +1,5 @@
 // Attention over the pages for few query rows (a decode step, drafted tokens): at
-// most 16 or 32 rows (token, head of the group) to a sequence and kv head.
+// most 16 rows (token, head of the group) to a sequence and kv head.
 //
 // Every key and value is read once and used for all the rows, some 2 x rows
 // flops a byte, so the cache's bytes bound it.  A page of 64 keys is a stage of
@@ -11,7 +11,7 @@
 //   P = 2^(c S - m), kept in registers: the accumulators of S are P's operand
 //   O += P V    mma m16n8k16 (K = 16 keys)
 //
-// (mma.sync, not tcgen05: 16 or 32 rows of its 128 would be used, and the
+// (mma.sync, not tcgen05: 16 rows of its 128 would be used, and the
 // operands come out of registers without a hand-over.)  An E4M3 cache is widened
 // to fp16 in registers (exact): two bytes of a key's fragment are neighbouring
 // channels, so Q is read with its channels in the same order; two bytes of a
@@ -37,6 +37,7 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kRows = 16;      // of an item
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kOver = 3;       // an item's start and end, in pages
@@ -44,21 +45,21 @@ constexpr int kMinPer = 6;     // least cost of a CTA's range
 constexpr int kSnap = 1;
 constexpr int kCtasPerSm = 2;
 
-template <int kDim, int kMode, int kMT>
+template <int kDim, int kMode>
 struct __align__(1024) Smem {
     static constexpr int kElem = is_e4m3(kMode) ? 1 : 2;
     static constexpr int kRowBytes = kDim * kElem < 128 ? kDim * kElem : 128;  // of a slab
     static constexpr int kSlabs = kDim * kElem / kRowBytes;
     static constexpr int kPageBytes = PAGE * kDim * kElem;
     static constexpr int kQStride = kDim * 2 + 16;
-    static constexpr int kRedBytes = 2 * 16 * kMT * kDim * 4;  // two warps' sums
-    static constexpr int kRoom = 112 * 1024 - kRedBytes - 16 * kMT * kQStride - 2048;
+    static constexpr int kRedBytes = 2 * kRows * kDim * 4;  // two warps' sums
+    static constexpr int kRoom = 112 * 1024 - kRedBytes - kRows * kQStride - 2048;
     static constexpr int kStages = kRoom / (2 * kPageBytes) < 12 ? kRoom / (2 * kPageBytes) : 12;
     uint8_t kv[kStages][2][kPageBytes];
-    uint8_t q[16 * kMT][kQStride];
-    float red[2][16 * kMT][kDim];
-    float ml[kWarps][16 * kMT][2];
-    float qc[16 * kMT];
+    uint8_t q[kRows][kQStride];
+    float red[2][kRows][kDim];
+    float ml[kWarps][kRows][2];
+    float qc[kRows];
     uint8_t bad[kStages];
     uint64_t full[kStages], empty[kStages];
     int abort;
@@ -113,14 +114,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
-template <int kMT>
-using Cursor = KvCursor<16 * kMT, PAGE, kOver>;
+using Cursor = KvCursor<kRows, PAGE, kOver>;
 
 // ---------------------------------------------------------------- loads
 
-template <int kDim, int kMode, int kMT>
-__device__ void role_load(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor<kMT> cur) {
-    using S = Smem<kDim, kMode, kMT>;
+template <int kDim, int kMode>
+__device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor cur) {
+    using S = Smem<kDim, kMode>;
     const int lane = threadIdx.x & 31;
     int st = 0;
     uint32_t phase = 0, used = 0;
@@ -166,13 +166,13 @@ __device__ void role_load(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvM
 
 // ---------------------------------------------------------------- rows
 
-template <int kDim, int kMode, int kMT>
-__device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g,
-                          Cursor<kMT> cur) {
-    using S = Smem<kDim, kMode, kMT>;
+template <int kDim, int kMode>
+__device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g,
+                          Cursor cur) {
+    using S = Smem<kDim, kMode>;
     constexpr bool kBf = kMode == kBf16;                           // operands
     constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;  // q and out
-    constexpr int kRows = 16 * kMT, kKs = kDim / 16, kNt = kDim / 8;
+    constexpr int kKs = kDim / 16, kNt = kDim / 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
     const float c0 = fmaxf(a.scale * kLog2e, FLT_MIN);
     int st = 0;
@@ -203,46 +203,41 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
             }
             warps_sync();
         }
-        uint32_t qf[kMT == 1 ? kKs : 1][4];
-        auto load_q = [&](int mt, int ks, uint32_t (&r)[4]) {
+        uint32_t qf[kKs][4];
+        auto load_q = [&](int ks, uint32_t (&r)[4]) {
             if constexpr (is_e4m3(kMode)) {  // channels 4 c .. 4 c + 3 of the 16
-                const uint2 x = *reinterpret_cast<const uint2*>(&sm.q[16 * mt + quad][32 * ks + 8 * qc]);
-                const uint2 y = *reinterpret_cast<const uint2*>(&sm.q[16 * mt + quad + 8][32 * ks + 8 * qc]);
+                const uint2 x = *reinterpret_cast<const uint2*>(&sm.q[quad][32 * ks + 8 * qc]);
+                const uint2 y = *reinterpret_cast<const uint2*>(&sm.q[quad + 8][32 * ks + 8 * qc]);
                 r[0] = x.x, r[1] = y.x, r[2] = x.y, r[3] = y.y;
             } else {
-                ldsm4(smem_u32(&sm.q[16 * mt + (lane & 15)][32 * ks + 16 * (lane >> 4)]), r);
+                ldsm4(smem_u32(&sm.q[lane & 15][32 * ks + 16 * (lane >> 4)]), r);
             }
         };
-        int pos[kMT][2], lo[kMT][2];
-        float cc[kMT][2], mref[kMT][2], l[kMT][2];
-        float o[kMT][kNt][4];
+        int pos[2], lo[2];
+        float cc[2], mref[2], l[2];
+        float o[kNt][4];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = min(16 * mt + quad + 8 * e, f.rows - 1);
-                pos[mt][e] = f.s.n - f.s.m + r / g;
-                lo[mt][e] = a.window > 0 ? max(0, pos[mt][e] - a.window + 1) : 0;
-                cc[mt][e] = kMode == kE4m3Bf16 && nb > 0 ? sm.qc[16 * mt + quad + 8 * e] : c0;
-                mref[mt][e] = -INFINITY, l[mt][e] = 0.0f;
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int r = min(quad + 8 * e, f.rows - 1);
+            pos[e] = f.s.n - f.s.m + r / g;
+            lo[e] = a.window > 0 ? max(0, pos[e] - a.window + 1) : 0;
+            cc[e] = kMode == kE4m3Bf16 && nb > 0 ? sm.qc[quad + 8 * e] : c0;
+            mref[e] = -INFINITY, l[e] = 0.0f;
+        }
         const int pos_min = f.s.n - f.s.m, lo_max = a.window > 0 ? max(0, f.v.hi - a.window + 1) : 0;
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+        for (int t = 0; t < kNt; ++t)
 #pragma unroll
-            for (int t = 0; t < kNt; ++t)
+            for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
+        if (nb > 0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.0f;
-        if constexpr (kMT == 1) {
-            if (nb > 0) {
-#pragma unroll
-                for (int ks = 0; ks < kKs; ++ks) load_q(0, ks, qf[ks]);
-            }
+            for (int ks = 0; ks < kKs; ++ks) load_q(ks, qf[ks]);
         }
         for (int j = f.f0; j < f.f1; ++j) {
-            if (!wait_bar_warp(sm, &sm.full[st], phase)) return;
+            // a wait that gave up does not end the loop: the warps meet at the same barriers
+            const bool there = wait_bar_warp(sm, &sm.full[st], phase);
             const int kb = j * PAGE + 16 * warp;  // the warp's keys
-            if (!sm.bad[st] && kb <= f.v.hi && kb + 15 >= f.v.lo) {
+            if (there && !sm.bad[st] && kb <= f.v.hi && kb + 15 >= f.v.lo) {
                 const uint32_t kp = smem_u32(sm.kv[st][0]), vp = smem_u32(sm.kv[st][1]);
                 const bool edge = kb + 15 > f.v.hi || kb < f.v.lo;
                 if (edge) {  // rows of V that no query sees: zero, as 0 x NaN is not
@@ -255,27 +250,19 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                     __syncwarp();
                 }
                 // ---- S
-                float s[kMT][2][4];
+                float s[2][4];
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
                 const int kr = 16 * warp + (lane & 7) + ((lane >> 4) << 3);  // ldmatrix row of this lane
                 if constexpr (!is_e4m3(kMode)) {
 #pragma unroll
                     for (int ks = 0; ks < kKs; ++ks) {
                         uint32_t b[4];
                         ldsm4(kp + at16<S>(kr, 2 * ks + ((lane >> 3) & 1)), b);
-#pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt) {
-                            uint32_t q2[4];
-                            if constexpr (kMT > 1) load_q(mt, ks, q2);
-                            const uint32_t(&q)[4] = kMT == 1 ? qf[kMT == 1 ? ks : 0] : q2;
-                            mma16816<kBf>(s[mt][0], q, b[0], b[1]);
-                            mma16816<kBf>(s[mt][1], q, b[2], b[3]);
-                        }
+                        mma16816<kBf>(s[0], qf[ks], b[0], b[1]);
+                        mma16816<kBf>(s[1], qf[ks], b[2], b[3]);
                     }
                 } else {
 #pragma unroll
@@ -283,70 +270,57 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                         uint32_t b[4];  // (keys 0-7, 16 channels), (keys 0-7, next 16), (keys 8-15, ..)
                         ldsm4(kp + at16<S>(kr, ks + ((lane >> 3) & 1)), b);
 #pragma unroll
-                        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-                            for (int mt = 0; mt < kMT; ++mt) {
-                                uint32_t q2[4];
-                                if constexpr (kMT > 1) load_q(mt, ks + k2, q2);
-                                const uint32_t(&q)[4] = kMT == 1 ? qf[kMT == 1 ? ks + k2 : 0] : q2;
-                                uint32_t w[4];
-                                e4m3x4_to_h2(b[k2], w[0], w[1]);
-                                e4m3x4_to_h2(b[2 + k2], w[2], w[3]);
-                                mma16816<false>(s[mt][0], q, w[0], w[1]);
-                                mma16816<false>(s[mt][1], q, w[2], w[3]);
-                            }
+                        for (int k2 = 0; k2 < 2; ++k2) {
+                            uint32_t w[4];
+                            e4m3x4_to_h2(b[k2], w[0], w[1]);
+                            e4m3x4_to_h2(b[2 + k2], w[2], w[3]);
+                            mma16816<false>(s[0], qf[ks + k2], w[0], w[1]);
+                            mma16816<false>(s[1], qf[ks + k2], w[2], w[3]);
+                        }
                     }
                 }
                 // ---- softmax: elements 0, 1 of row quad, 2, 3 of row quad + 8
                 if (kb + 15 > pos_min || kb < lo_max) {
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int key = kb + 8 * t + 2 * qc + (e & 1);
-                                if (key > pos[mt][e >> 1] || key < lo[mt][e >> 1]) s[mt][t][e] = -INFINITY;
-                            }
-                }
-                float bm[kMT][2];
-                bool move = false;
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]), fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        bm[mt][e] = x * cc[mt][e];
-                        move = move || bm[mt][e] > mref[mt][e] + kGap || (mref[mt][e] == -INFINITY && bm[mt][e] > -INFINITY);
-                    }
-                if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float mn = fmaxf(mref[mt][e], bm[mt][e]);
-                            const float x = mn == -INFINITY ? 1.0f : ex2(mref[mt][e] - mn);
-                            mref[mt][e] = mn;
-                            l[mt][e] *= x;
-#pragma unroll
-                            for (int t = 0; t < kNt; ++t) o[mt][t][2 * e] *= x, o[mt][t][2 * e + 1] *= x;
-                        }
-                }
-                uint32_t p[kMT][4];
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float ms = mref[mt][e] == -INFINITY ? 0.0f : mref[mt][e];
-                            const float x = ex2(fmaf(s[mt][t][2 * e], cc[mt][e], -ms));
-                            const float y = ex2(fmaf(s[mt][t][2 * e + 1], cc[mt][e], -ms));
-                            l[mt][e] += x + y;
-                            p[mt][2 * t + e] = pack16(x, y, kBf);
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = kb + 8 * t + 2 * qc + (e & 1);
+                            if (key > pos[e >> 1] || key < lo[e >> 1]) s[t][e] = -INFINITY;
                         }
+                }
+                float bm[2];
+                bool move = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    bm[e] = x * cc[e];
+                    move = move || bm[e] > mref[e] + kGap || (mref[e] == -INFINITY && bm[e] > -INFINITY);
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(mref[e], bm[e]);
+                        const float x = mn == -INFINITY ? 1.0f : ex2(mref[e] - mn);
+                        mref[e] = mn;
+                        l[e] *= x;
+#pragma unroll
+                        for (int t = 0; t < kNt; ++t) o[t][2 * e] *= x, o[t][2 * e + 1] *= x;
+                    }
+                }
+                uint32_t p[4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float ms = mref[e] == -INFINITY ? 0.0f : mref[e];
+                        const float x = ex2(fmaf(s[t][2 * e], cc[e], -ms));
+                        const float y = ex2(fmaf(s[t][2 * e + 1], cc[e], -ms));
+                        l[e] += x + y;
+                        p[2 * t + e] = pack16(x, y, kBf);
+                    }
                 // ---- O
                 const int vr = 16 * warp + (lane & 15);
                 if constexpr (!is_e4m3(kMode)) {
@@ -354,11 +328,8 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                     for (int t = 0; t < kNt; t += 2) {
                         uint32_t b[4];  // (keys 0-7, 8 channels), (keys 8-15, ..), the next 8 channels
                         ldsm4t(vp + at16<S>(vr, t + (lane >> 4)), b);
-#pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt) {
-                            mma16816<kBf>(o[mt][t], p[mt], b[0], b[1]);
-                            mma16816<kBf>(o[mt][t + 1], p[mt], b[2], b[3]);
-                        }
+                        mma16816<kBf>(o[t], p, b[0], b[1]);
+                        mma16816<kBf>(o[t + 1], p, b[2], b[3]);
                     }
                 } else {
 #pragma unroll
@@ -371,11 +342,8 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
                             uint32_t e0, e1, d0, d1;
                             e4m3x4_to_h2(__byte_perm(b[2 * u], 0, 0x3120), e0, d0);
                             e4m3x4_to_h2(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, d1);
-#pragma unroll
-                            for (int mt = 0; mt < kMT; ++mt) {
-                                mma16816<false>(o[mt][t + 2 * u], p[mt], e0, e1);
-                                mma16816<false>(o[mt][t + 2 * u + 1], p[mt], d0, d1);
-                            }
+                            mma16816<false>(o[t + 2 * u], p, e0, e1);
+                            mma16816<false>(o[t + 2 * u + 1], p, d0, d1);
                         }
                     }
                 }
@@ -386,54 +354,48 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
         }
         // ---- the warps' sums over their keys, joined in a fixed order
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-                l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
-                if (qc == 0) {
-                    sm.ml[warp][16 * mt + quad + 8 * e][0] = mref[mt][e];
-                    sm.ml[warp][16 * mt + quad + 8 * e][1] = l[mt][e];
-                }
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (qc == 0) {
+                sm.ml[warp][quad + 8 * e][0] = mref[e];
+                sm.ml[warp][quad + 8 * e][1] = l[e];
             }
+        }
         warps_sync();
-        float w[kMT][2];  // weight of this warp's sums
+        float w[2];  // weight of this warp's sums
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 16 * mt + quad + 8 * e;
-                const float M = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
-                w[mt][e] = M == -INFINITY ? 0.0f : ex2(mref[mt][e] - M);
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int r = quad + 8 * e;
+            const float M = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
+            w[e] = M == -INFINITY ? 1.0f : ex2(mref[e] - M);  // no key seen: zeros, or NaN scores' NaN
+        }
         // channel of element e of accumulator t: neighbouring pairs, but for E4M3 every other one
         auto place = [&](bool add, int buf) {
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int t = 0; t < kNt; t += is_e4m3(kMode) ? 2 : 1)
 #pragma unroll
-                for (int t = 0; t < kNt; t += is_e4m3(kMode) ? 2 : 1)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float* row = sm.red[buf][16 * mt + quad + 8 * e];
-                        if constexpr (is_e4m3(kMode)) {
-                            float4* d = reinterpret_cast<float4*>(row + 8 * t + 4 * qc);
-                            float4 v = make_float4(o[mt][t][2 * e], o[mt][t + 1][2 * e], o[mt][t][2 * e + 1], o[mt][t + 1][2 * e + 1]);
-                            v.x *= w[mt][e], v.y *= w[mt][e], v.z *= w[mt][e], v.w *= w[mt][e];
-                            if (add) {
-                                const float4 u = *d;
-                                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-                            }
-                            *d = v;
-                        } else {
-                            float2* d = reinterpret_cast<float2*>(row + 8 * t + 2 * qc);
-                            float2 v = make_float2(o[mt][t][2 * e] * w[mt][e], o[mt][t][2 * e + 1] * w[mt][e]);
-                            if (add) {
-                                const float2 u = *d;
-                                v.x += u.x, v.y += u.y;
-                            }
-                            *d = v;
+                for (int e = 0; e < 2; ++e) {
+                    float* row = sm.red[buf][quad + 8 * e];
+                    if constexpr (is_e4m3(kMode)) {
+                        float4* d = reinterpret_cast<float4*>(row + 8 * t + 4 * qc);
+                        float4 v = make_float4(o[t][2 * e], o[t + 1][2 * e], o[t][2 * e + 1], o[t + 1][2 * e + 1]);
+                        v.x *= w[e], v.y *= w[e], v.z *= w[e], v.w *= w[e];
+                        if (add) {
+                            const float4 u = *d;
+                            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
                         }
+                        *d = v;
+                    } else {
+                        float2* d = reinterpret_cast<float2*>(row + 8 * t + 2 * qc);
+                        float2 v = make_float2(o[t][2 * e] * w[e], o[t][2 * e + 1] * w[e]);
+                        if (add) {
+                            const float2 u = *d;
+                            v.x += u.x, v.y += u.y;
+                        }
+                        *d = v;
                     }
+                }
         };
         if (warp < 2) place(false, warp);
         warps_sync();
@@ -448,7 +410,7 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm.ml[k][r][0]);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) L += M == -INFINITY ? 0.0f : sm.ml[k][r][1] * ex2(sm.ml[k][r][0] - M);
+            for (int k = 0; k < kWarps; ++k) L += sm.ml[k][r][1] * (M == -INFINITY ? 1.0f : ex2(sm.ml[k][r][0] - M));
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
@@ -475,17 +437,17 @@ __device__ void role_rows(Smem<kDim, kMode, kMT>& sm, const KvAttn& a, const KvP
             }
         }
         if (!whole && f.first && threadIdx.x == 0)
-            parts.cut[blockIdx.x] = kv_cut<kSnap>(f, blockIdx.x, per, g, 16 * kMT);
+            parts.cut[blockIdx.x] = kv_cut<kSnap>(f, blockIdx.x, per, g, kRows);
         warps_sync();  // the buffers are free for the next item
     }
 }
 
-template <int kDim, int kMode, int kMT>
+template <int kDim, int kMode>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     k_kv_rows(const __grid_constant__ KvAttn a, const __grid_constant__ KvMaps maps, const __grid_constant__ KvPlan plan,
               const __grid_constant__ KvParts parts) {
     extern __shared__ uint8_t smem_raw[];
-    using S = Smem<kDim, kMode, kMT>;
+    using S = Smem<kDim, kMode>;
     S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     static_assert(sizeof(KvPlanSmem) <= sizeof(sm.kv), "the plan's arrays lie in the ring");
     if (threadIdx.x == 0) {
@@ -500,19 +462,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     cudaGridDependencySynchronize();
     if (threadIdx.x == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
-    const Cursor<kMT> cur = kv_plan<16 * kMT, PAGE, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    const Cursor cur = kv_plan<kRows, PAGE, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     __syncthreads();
-    if (threadIdx.x < 32 * kWarps) role_rows<kDim, kMode, kMT>(sm, a, parts, per, plan.g, cur);
-    else role_load<kDim, kMode, kMT>(sm, a, maps, plan.g, cur);
+    if (threadIdx.x < 32 * kWarps) role_rows<kDim, kMode>(sm, a, parts, per, plan.g, cur);
+    else role_load<kDim, kMode>(sm, a, maps, plan.g, cur);
     __syncwarp();
     __syncthreads();
     if (sm.abort && threadIdx.x == 0) atomicOr(a.c.status, CSA2_DEVERR_TIMEOUT);
 }
 
-template <int kDim, int kMode, int kMT>
+template <int kDim, int kMode>
 cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
-    using S = Smem<kDim, kMode, kMT>;
+    using S = Smem<kDim, kMode>;
     constexpr int kSmem = sizeof(S) + 1024;
     static_assert(kCtasPerSm * (kSmem + 1024) <= 233472, "two CTAs an SM");
     static_assert(S::kStages >= 2, "a ring");
@@ -527,34 +489,29 @@ cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
     plan.g = a.H / a.c.kv_heads;
     plan.grid = kCtasPerSm * device_sm_count();
     plan.min_per = kMinPer;
-    const KvParts parts = kv_parts(a.ws, plan.grid, 16 * kMT, kDim);
+    const KvParts parts = kv_parts(a.ws, plan.grid, kRows, kDim);
     static std::atomic<uint64_t> attr_done{0};
-    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_rows<kDim, kMode, kMT>), kSmem, attr_done);
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_rows<kDim, kMode>), kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    e = launch_behind(k_kv_rows<kDim, kMode, kMT>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
+    e = launch_behind(k_kv_rows<kDim, kMode>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
     if (e != cudaSuccess) return e;
     constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
-    return launch_behind(k_kv_join<kDim, kOutBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, 16 * kMT, plan.grid);
-}
-
-template <int kDim, int kMode>
-cudaError_t rows_mode(const KvAttn& a, cudaStream_t st) {
-    return kv_rows_tile(a.max_new, a.H / a.c.kv_heads) == 16 ? rows_as<kDim, kMode, 1>(a, st) : rows_as<kDim, kMode, 2>(a, st);
+    return launch_behind(k_kv_join<kDim, kOutBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, kRows, plan.grid);
 }
 
 }  // namespace
 
-size_t kv_rows_workspace_bytes(int tile, int head_dim) {
-    return kv_parts_bytes(kCtasPerSm * device_sm_count(), tile, head_dim);
+size_t kv_rows_workspace_bytes(int head_dim) {
+    return kv_parts_bytes(kCtasPerSm * device_sm_count(), kRows, head_dim);
 }
 
 cudaError_t launch_kv_rows(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st) {
     const bool e4m3 = kv_dtype == CSA2_KV_E4M3, bf = dtype == CSA2_DTYPE_BF16;
     if (head_dim == 64)
-        return e4m3 ? (bf ? rows_mode<64, kE4m3Bf16>(a, st) : rows_mode<64, kE4m3F16>(a, st))
-                    : (bf ? rows_mode<64, kBf16>(a, st) : rows_mode<64, kF16>(a, st));
-    return e4m3 ? (bf ? rows_mode<128, kE4m3Bf16>(a, st) : rows_mode<128, kE4m3F16>(a, st))
-                : (bf ? rows_mode<128, kBf16>(a, st) : rows_mode<128, kF16>(a, st));
+        return e4m3 ? (bf ? rows_as<64, kE4m3Bf16>(a, st) : rows_as<64, kE4m3F16>(a, st))
+                    : (bf ? rows_as<64, kBf16>(a, st) : rows_as<64, kF16>(a, st));
+    return e4m3 ? (bf ? rows_as<128, kE4m3Bf16>(a, st) : rows_as<128, kE4m3F16>(a, st))
+                : (bf ? rows_as<128, kBf16>(a, st) : rows_as<128, kF16>(a, st));
 }
 
 }  // namespace csa2

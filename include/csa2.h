@@ -603,7 +603,11 @@ int csa2_kv_append(const csa2_kv_cache* cache, const csa2_heads* k, const csa2_h
                    int total, int max_new, const int32_t* start, const csa2_rotary* rot, const int32_t* pos,
                    csa2_stream stream);
 
-/* Workspace bytes csa2_kv_attn needs for these sizes (0: sizes that it refuses). */
+/*
+ * Workspace bytes csa2_kv_attn needs for these sizes (0: sizes that it refuses) on
+ * the current device.  What does for max_new new tokens does for fewer.  It needs no
+ * initial value and belongs to one call at a time.
+ */
 size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new, int H);
 
 /*
