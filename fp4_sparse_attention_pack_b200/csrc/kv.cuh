@@ -86,7 +86,7 @@ struct KvAttn {
     int H, total, max_new, window;
     float scale;
 };
-size_t kv_attn_workspace_bytes(int max_new, int H, int kv_heads, int head_dim);
+size_t kv_attn_workspace_bytes(int max_new, int H, const csa2_kv_cache& c);
 cudaError_t launch_kv_attn(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st);
 
 }  // namespace csa2

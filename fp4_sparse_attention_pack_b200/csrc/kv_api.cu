@@ -147,7 +147,7 @@ int csa2_kv_append(const csa2_kv_cache* cache, const csa2_heads* k, const csa2_h
 
 size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new, int H) {
     if (check_kv_cache(cache) || total < 0 || max_new < 0 || H < 1 || H > CSA2_MAX_H || H % cache->kv_heads) return 0;
-    return kv_attn_workspace_bytes(max_new, H, cache->kv_heads, cache->head_dim);
+    return kv_attn_workspace_bytes(max_new, H, *cache);
 }
 
 int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dtype, const int32_t* cu, int total,
@@ -164,7 +164,7 @@ int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dty
         return rc;
     if (q->data == out->data) return CSA2_ERR_INVALID_ARG;
     if (!a16(cu) || !a16(lse) || !a16(ws)) return CSA2_ERR_ALIGN;
-    const size_t need = kv_attn_workspace_bytes(max_new, H, cache->kv_heads, cache->head_dim);
+    const size_t need = kv_attn_workspace_bytes(max_new, H, *cache);
     if (need > 0 && (!ws || ws_bytes < need)) return CSA2_ERR_WORKSPACE;
     if (inject_fault("csa2_kv_attn")) return CSA2_ERR_CUDA;
     KvAttn a;

@@ -216,9 +216,18 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_
 }  // namespace
 
 // Calls of at most 16 rows to an item go to the few-rows kernel.  (One token of 8
-// sequences over 32,768, 64 / 8 heads of 128: 177 us there, 199 us in the chunk
-// kernel; over an E4M3 cache of 65,536 229 and 339 us.  Two tiles of 16 rows in it,
-// 4 tokens each: 348 us against 192 us in the chunk kernel.)
+// sequences over 32,768, 64 / 8 heads of 128: 172 us there, 199 us in the chunk
+// kernel; heads of 64: 100 and 143 us.  Two tiles of 16 rows in it, 4 tokens each:
+// 348 us against 183 us in the chunk kernel.)
 inline bool kv_few_rows(int max_new, int g) { return (int64_t)max_new * g <= 16; }
+
+// Calls over E4M3 pages of 128 channels with at most 32 rows to an item: the tensor
+// cores read the codes.  (8 sequences over 65,536, 64 / 8 heads: one token 192 us
+// against 229 us with codes widened in the few-rows kernel's registers, 4 tokens 227
+// against 393 us with codes widened in the chunk kernel's shared memory.  More rows
+// would need more than 3 x 32 columns of each product in TMEM.)
+inline bool kv_codes(int max_new, int g, int head_dim, int kv_dtype) {
+    return kv_dtype == CSA2_KV_E4M3 && head_dim == 128 && (int64_t)max_new * g <= 32;
+}
 
 }  // namespace csa2

@@ -3,7 +3,7 @@
 //
 // Every key and value is read once and used for all the rows, some 2 x rows
 // flops a byte, so the cache's bytes bound it.  A page of 64 keys is a stage of
-// a TMA ring (about 96 KB in flight in each of two CTAs an SM); warp w of four
+// a TMA ring (64 to 92 KB of pages in each of two CTAs an SM); warp w of four
 // takes its keys 16 w .. 16 w + 15 with an online softmax of its own, so the
 // warps meet only at an item's end:
 //
@@ -12,13 +12,18 @@
 //   O += P V    mma m16n8k16 (K = 16 keys)
 //
 // (mma.sync, not tcgen05: 16 rows of its 128 would be used, and the
-// operands come out of registers without a hand-over.)  An E4M3 cache is widened
+// operands come out of registers without a hand-over.)  An E4M3 cache (heads of 64;
+// kv_codes.cu takes those of 128) is widened
 // to fp16 in registers (exact): two bytes of a key's fragment are neighbouring
 // channels, so Q is read with its channels in the same order; two bytes of a
 // value's (transposed) fragment are two channels of one key, which byte
 // permutations pair by key.  Queries are scaled per row as in kv_mma.cu.
 // The work is cut evenly over the CTAs (kv_plan.cuh), which splits long
 // sequences when there are few.
+//
+// One token of 16 sequences to 32,768, 64 / 8 heads of 128, bf16: 209 us (6.3 TB/s,
+// 98% of the copy rate); heads of 64: 83%, and 51% over E4M3 pages, where the
+// conversions and the byte permutations of half as many bytes take as long.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -505,13 +510,15 @@ size_t kv_rows_workspace_bytes(int head_dim) {
     return kv_parts_bytes(kCtasPerSm * device_sm_count(), kRows, head_dim);
 }
 
+// E4M3 pages: heads of 64 (kv_codes.cu takes those of 128).
 cudaError_t launch_kv_rows(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st) {
-    const bool e4m3 = kv_dtype == CSA2_KV_E4M3, bf = dtype == CSA2_DTYPE_BF16;
-    if (head_dim == 64)
-        return e4m3 ? (bf ? rows_as<64, kE4m3Bf16>(a, st) : rows_as<64, kE4m3F16>(a, st))
-                    : (bf ? rows_as<64, kBf16>(a, st) : rows_as<64, kF16>(a, st));
-    return e4m3 ? (bf ? rows_as<128, kE4m3Bf16>(a, st) : rows_as<128, kE4m3F16>(a, st))
-                : (bf ? rows_as<128, kBf16>(a, st) : rows_as<128, kF16>(a, st));
+    const bool bf = dtype == CSA2_DTYPE_BF16;
+    if (kv_dtype == CSA2_KV_E4M3) {
+        if (head_dim != 64) return cudaErrorInvalidValue;
+        return bf ? rows_as<64, kE4m3Bf16>(a, st) : rows_as<64, kE4m3F16>(a, st);
+    }
+    if (head_dim == 64) return bf ? rows_as<64, kBf16>(a, st) : rows_as<64, kF16>(a, st);
+    return bf ? rows_as<128, kBf16>(a, st) : rows_as<128, kF16>(a, st);
 }
 
 }  // namespace csa2
