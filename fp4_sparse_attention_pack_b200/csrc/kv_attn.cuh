@@ -221,13 +221,14 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_
 // 348 us against 183 us in the chunk kernel.)
 inline bool kv_few_rows(int max_new, int g) { return (int64_t)max_new * g <= 16; }
 
-// Calls over E4M3 pages of 128 channels with at most 32 rows to an item: the tensor
-// cores read the codes.  (8 sequences over 65,536, 64 / 8 heads: one token 192 us
-// against 229 us with codes widened in the few-rows kernel's registers, 4 tokens 227
-// against 393 us with codes widened in the chunk kernel's shared memory.  More rows
-// would need more than 3 x 32 columns of each product in TMEM.)
-inline bool kv_codes(int max_new, int g, int head_dim, int kv_dtype) {
-    return kv_dtype == CSA2_KV_E4M3 && head_dim == 128 && (int64_t)max_new * g <= 32;
+// Calls over E4M3 pages with at most 32 rows to an item: the tensor cores read the
+// codes.  (8 sequences over 65,536, 64 / 8 heads of 128: one token 176 us against 229
+// us with codes widened in the few-rows kernel's registers, 4 tokens 215 against 393
+// us with codes widened in the chunk kernel's shared memory; heads of 64: 130 against
+// 162 and 193 against 303 us.  More rows would need more than 3 x 32 columns of each
+// product in TMEM.)
+inline bool kv_codes(int max_new, int g, int kv_dtype) {
+    return kv_dtype == CSA2_KV_E4M3 && (int64_t)max_new * g <= 32;
 }
 
 }  // namespace csa2

@@ -1,7 +1,6 @@
 // Attention over E4M3 pages for few query rows (at most 16 or 32 rows of token x head
-// of the group to a sequence and kv head), heads of 128 channels: the tensor cores
-// read the codes themselves (tcgen05.mma kind::f8f6f4, fp32 accumulation in TMEM), so
-// no page is widened.
+// of the group to a sequence and kv head): the tensor cores read the codes themselves
+// (tcgen05.mma kind::f8f6f4, fp32 accumulation in TMEM), so no page is widened.
 //
 // Keys and values are the operand with 128 rows, queries and probabilities the one
 // with N columns, each split into three E4M3 terms of four bits (12 bits together,
@@ -21,12 +20,14 @@
 //                   = channel (lane of O^T).  The maxima in use move only when a score
 //                   exceeds one by more than 8 (log2).
 //   warp 8          issues the MMAs;
-//   warp 9          loads pages by TMA, K a block ahead of V;
-//   warps 10, 11    load and split the queries and tell the others which item is next.
+//   warps 9, 11     load pages by TMA, K and V (one warp for both took 1,600 cycles a
+//                   block, more than the bytes);
+//   warp 10         loads and splits the queries and tells the others which item is next.
 //
-// The cache's bytes bound it: one token of 8 sequences over 65,536, 64 / 8 heads, takes
-// 192 us (5.6 TB/s, 87% of the copy rate); with 32 rows (4 tokens each) the softmax
-// warps' instructions, some 470 a thread and block, bring it to 227 us (73%).
+// The cache's bytes bound it: one token of 8 sequences over 65,536, 64 / 8 heads of
+// 128, takes 176 us (6.1 TB/s, 94% of the copy rate); with 32 rows (4 tokens each) the
+// softmax warps' instructions, some 470 a thread and block, bring it to 215 us (77%),
+// and heads of 64, whose blocks have half the bytes, to 130 and 193 us (64%, 43%).
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -42,7 +43,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kDim = 128;
 constexpr int kBlk = 128;    // keys of a block
 constexpr int kOver = 2;     // an item's start and end, in blocks
 constexpr int kMinPer = 4;   // least cost of a CTA's range
@@ -53,17 +53,18 @@ template <int R>
 constexpr int kRegsSoftmax = R == 32 ? 200 : kRegsLaunch;
 template <int R>
 constexpr int kRegsOther = R == 32 ? 104 : kRegsLaunch;
-constexpr int kWarpMma = 8, kWarpTma = 9, kWarpQ = 10;
-constexpr int kPlaces = 10;  // of 16 KB, K and V blocks in the order of their use
+constexpr int kWarpMma = 8, kWarpK = 9, kWarpQ = 10, kWarpV = 11;
+constexpr int places_of(int dim) { return dim == 64 ? 16 : 10; }  // K and V blocks in the order of their use
 constexpr int kRing = 16;    // blocks whose masks of bad pages are kept
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // two of each, 128 columns apart
 constexpr float kNone = -FLT_MAX / 2;                         // maximum in use before any
 
-template <int R>
+template <int kDim, int R>
 struct Smem {
-    alignas(16) uint8_t kv[kPlaces][kBlk * 128];  // [key][128 codes], SW128
+    static constexpr int kPlaces = places_of(kDim);
+    alignas(16) uint8_t kv[kPlaces][kBlk * kDim];  // [key][channel], swizzled by its width
     uint8_t p[2][kBlk * 128];                     // [key][3 R codes], SW128
-    uint8_t q[3 * R * 128];                       // [term][row][128 codes], SW128
+    uint8_t q[3 * R * kDim];                      // [term][row][channel], as kv
     float4 cm[2][R / 2];                          // (c, -maximum) of two rows each
     float factor[2][R];
     float wmax[2][4][32], wsum[2][4][32];
@@ -80,7 +81,11 @@ struct Smem {
     int abort;
 };
 
-__device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+// Byte offset of 16-byte chunk c of row r of `width` bytes with the swizzle of that width.
+template <int width>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    return width == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
 
 // Bounded wait of a warp that also gives up when another role has given up.
 template <class S>
@@ -139,25 +144,29 @@ __device__ __forceinline__ void split(uint32_t h, uint32_t (&e)[3]) {
 
 // ---------------------------------------------------------------- MMA
 
-template <int R>
-__device__ void role_mma(Smem<R>& sm, uint32_t tb) {
+template <int kDim, int R>
+__device__ void role_mma(Smem<kDim, R>& sm, uint32_t tb) {
     // kind::f8f6f4 has the fields of kind::f16; format 0 is E4M3
     const uint32_t idesc_s = idesc_f16(128, 3 * R, 0, 0, 0), idesc_o = idesc_f16(128, 3 * R, 0, 1, 1);
-    const uint64_t desc_q = smem_desc(sm.q, 16, 1024, kLayoutSw128);
-    const uint64_t desc_kv = smem_desc(sm.kv[0], 16, 1024, kLayoutSw128);
+    constexpr uint32_t kLayout = kDim == 128 ? kLayoutSw128 : kLayoutSw64;
+    const uint64_t desc_q = smem_desc(sm.q, 16, 8 * kDim, kLayout);
+    const uint64_t desc_k = smem_desc(sm.kv[0], 16, 8 * kDim, kLayout);
+    // heads of 64: the product has 128 rows all the same, those behind the 64th come
+    // from what lies behind the block, and nothing reads them
+    const uint64_t desc_v = smem_desc(sm.kv[0], kBlk * kDim, 8 * kDim, kLayout);
     const uint64_t desc_p = smem_desc(sm.p[0], 16, 1024, kLayoutSw128);
     int place = 0;
     uint32_t phase = 0, items = 0, np[2] = {0, 0};
     auto step = [&] {
         tc_commit_w(&sm.empty[place]);
-        if (++place == kPlaces) place = 0, phase ^= 1;
+        if (++place == Smem<kDim, R>::kPlaces) place = 0, phase ^= 1;
     };
     auto scores = [&](int t) {  // S_t^T = K q^T
         if (!wait_bar(sm, &sm.full[place], phase)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            tc_mma_f8_w(tb + kColS + 128 * t, desc_kv + (uint32_t)(place * (kBlk * 128) >> 4) + 2 * ks, desc_q + 2 * ks, idesc_s, ks > 0);
+        for (int ks = 0; ks < kDim / 32; ++ks)
+            tc_mma_f8_w(tb + kColS + 128 * t, desc_k + (uint32_t)(place * (kBlk * kDim) >> 4) + 2 * ks, desc_q + 2 * ks, idesc_s, ks > 0);
         tc_commit_w(&sm.s_full[t]);
         step();
         return true;
@@ -182,7 +191,7 @@ __device__ void role_mma(Smem<R>& sm, uint32_t tb) {
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)  // O_t^T += V^T p, 32 keys at a time
-                tc_mma_f8_w(tb + kColO + 128 * t, desc_kv + (uint32_t)((place * (kBlk * 128) + ks * 4096) >> 4),
+                tc_mma_f8_w(tb + kColO + 128 * t, desc_v + (uint32_t)((place * (kBlk * kDim) + ks * 32 * kDim) >> 4),
                             desc_p + (uint32_t)((t * (kBlk * 128) + ks * 4096) >> 4), idesc_o, j > 1 || ks > 0);
             step();
             if (j + 2 < nb) {
@@ -197,128 +206,123 @@ __device__ void role_mma(Smem<R>& sm, uint32_t tb) {
 
 // ---------------------------------------------------------------- loads
 
-template <int R>
-__device__ void role_tma(Smem<R>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor<R> cur) {
-    constexpr int kPage = PAGE * kDim;
+// The ring holds K0 K1 V0 K2 V1 .. of an item's nb blocks, the order of their use.
+__device__ __forceinline__ int place_in_item(int j, int nb, bool is_v) {
+    if (is_v) return j == nb - 1 ? 2 * nb - 1 : 2 * j + 2;
+    return j == 0 ? 0 : 2 * j - 1;
+}
+
+template <int kDim, int R, bool kV>
+__device__ void role_tma(Smem<kDim, R>& sm, const KvAttn& a, const KvMaps& maps, int g, Cursor<R> cur) {
+    constexpr int kPage = PAGE * kDim, kPlaces = Smem<kDim, R>::kPlaces;
     const int lane = threadIdx.x & 31;
-    int place = 0;
-    uint32_t phase = 0, used = 0, tails = 0, blocks = 0;
+    uint32_t base = 0, tails = 0, blocks = 0;
+    uint32_t issued = 0, parity = 0;  // places that this warp filled, and in which turn of the ring
     KvFrag f;
-    struct Pages {
-        int p[2], bad;
-    } pp = {{-1, -1}, 0};
-    auto load = [&](const Pages& pg, bool is_v, uint64_t* bar) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (pg.p[i] >= 0)
-                tma_load_2d_nohint_w(&sm.kv[place][i * kPage], is_v ? &maps.v : &maps.k, 0, (pg.p[i] * a.c.kv_heads + f.h) * PAGE, bar);
-    };
-    auto put = [&](const Pages& pg, int j, uint32_t block, bool is_v) {
-        if (used >= kPlaces && !wait_bar(sm, &sm.empty[place], phase ^ 1)) return false;
-        ++used;
-        uint64_t* full = &sm.full[place];
-        const uint32_t bytes = ((pg.p[0] >= 0) + (pg.p[1] >= 0)) * kPage;
-        if (!is_v) {
-            if (lane == 0) {
-                sm.bad[block % kRing] = (uint8_t)pg.bad;
-                if (pg.bad) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
-            }
-            __syncwarp();
-        }
-        if (!is_v || (j * kBlk >= f.v.lo && j * kBlk + kBlk - 1 <= f.v.hi && !pg.bad)) {
-            mbar_expect_tx_w(full, bytes);
-            load(pg, is_v, full);
-        } else {  // rows of V that no query sees: zero, as 0 x NaN is not
-            if (bytes) {
-                mbar_expect_tx_w(&sm.tail, bytes);
-                load(pg, true, &sm.tail);
-                // its own copy: waited for even when the others have given up
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
-                    atomicExch(&sm.abort, 1);
-                    return false;
-                }
-                ++tails;
-            }
-            for (int i = lane; i < kBlk * 8; i += 32) {
-                const int r = i >> 3, key = j * kBlk + r;
-                if (key < f.v.lo || key > f.v.hi || (pg.bad >> (r >> 6) & 1))
-                    *reinterpret_cast<uint4*>(&sm.kv[place][r * 128 + (i & 7) * 16]) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            mbar_arrive_w(full);
-        }
-        if (++place == kPlaces) place = 0, phase ^= 1;
-        return true;
-    };
     bool alive = true;
     while (alive && cur.next(a, g, f)) {
         const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
         const int nb = f.f1 - f.f0, first = f.v.lo / PAGE, last = f.v.hi / PAGE;
         int ids = -1, have = -1;  // 32 page ids at a time, one to a lane
-        for (int x = -1; x < nb && alive; ++x) {  // K of block x + 1, then V of block x
-            const Pages before = pp;
-            if (x + 1 < nb) {
-                const int j = f.f0 + x + 1;
-                if (have != 2 * j / 32) {
-                    have = 2 * j / 32;
-                    const int pg = 32 * have + lane;
-                    ids = pg >= first && pg <= last ? table[pg] : -1;
-                }
-                pp.bad = 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (2 * j + i) & 31), pg = 2 * j + i;
-                    const bool need = pg >= first && pg <= last, good = id >= 0 && id < a.c.num_pages;
-                    pp.p[i] = need && good ? id : -1;
-                    if (need && !good) pp.bad |= 1 << i;
-                }
-                alive = put(pp, j, blocks + x + 1, false);
+        for (int x = 0; x < nb && alive; ++x) {
+            const int j = f.f0 + x;
+            if (have != 2 * j / 32) {
+                have = 2 * j / 32;
+                const int pg = 32 * have + lane;
+                ids = pg >= first && pg <= last ? table[pg] : -1;
             }
-            if (x >= 0 && alive) alive = put(before, f.f0 + x, 0, true);
+            int page[2], bad = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int id = __shfl_sync(0xffffffffu, ids, (2 * j + i) & 31), pg = 2 * j + i;
+                const bool need = pg >= first && pg <= last, good = id >= 0 && id < a.c.num_pages;
+                page[i] = need && good ? id : -1;
+                if (need && !good) bad |= 1 << i;
+            }
+            const uint32_t at = base + place_in_item(x, nb, kV), turn = at / kPlaces;
+            const int place = at % kPlaces;
+            if (turn > 0 && !(alive = wait_bar(sm, &sm.empty[place], (turn - 1) & 1))) break;
+            if (!kV) {
+                if (lane == 0) {
+                    sm.bad[(blocks + x) % kRing] = (uint8_t)bad;
+                    if (bad) atomicOr(a.c.status, CSA2_DEVERR_PAGE);
+                }
+                __syncwarp();
+            }
+            // rows of V that no query sees are zeroed when they are there, as 0 x NaN is not 0
+            const bool part = kV && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
+            uint64_t* bar = part ? &sm.tail : &sm.full[place];
+            const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * kPage;
+            if (!part || bytes) {
+                mbar_expect_tx_w(bar, bytes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (page[i] >= 0)
+                        tma_load_2d_nohint_w(&sm.kv[place][i * kPage], kV ? &maps.v : &maps.k, 0, (page[i] * a.c.kv_heads + f.h) * PAGE, bar);
+            }
+            if (!part) {
+                issued |= 1u << place;
+                parity = (parity & ~(1u << place)) | (turn & 1) << place;
+                continue;
+            }
+            if (bytes) {
+                // its own copy: waited for even when the others have given up
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.tail, tails & 1))) {
+                    atomicExch(&sm.abort, 1);
+                    alive = false;
+                    break;
+                }
+                ++tails;
+            }
+            for (int i = lane; i < kBlk * kDim / 16; i += 32) {
+                const int r = i / (kDim / 16), key = j * kBlk + r;
+                if (key < f.v.lo || key > f.v.hi || (bad >> (r >> 6) & 1))
+                    *reinterpret_cast<uint4*>(&sm.kv[place][16 * i]) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_w(&sm.full[place]);
         }
+        base += 2 * nb;
         blocks += nb;
     }
     // no copy is in flight when the CTA ends, also after a wait that gave up
     if (*reinterpret_cast<volatile int*>(&sm.abort)) {
-        for (uint32_t k = 0; k < min(used, (uint32_t)kPlaces); ++k) {
-            const int st = (place + kPlaces - 1 - (int)k) % kPlaces;
-            (void)mbar_wait(&sm.full[st], st < place ? phase : phase ^ 1);
-        }
+        for (int p = 0; p < kPlaces; ++p)
+            if (issued >> p & 1) (void)mbar_wait(&sm.full[p], parity >> p & 1);
     }
 }
 
 // Queries: a pair of lanes to a row, every other eight channels each.
-template <int R, bool kBf>
-__device__ void role_q(Smem<R>& sm, const KvAttn& a, int g, Cursor<R> cur) {
+template <int kDim, int R, bool kBf>
+__device__ void role_q(Smem<kDim, R>& sm, const KvAttn& a, int g, Cursor<R> cur) {
     const int tid = threadIdx.x - 32 * kWarpQ, odd = tid & 1;
     const float c0 = fmaxf(a.scale * kLog2e, FLT_MIN);
     uint32_t items = 0;
     KvFrag f;
     for (uint32_t n = 0;; ++n) {
         const bool more = cur.next(a, g, f);
-        if (tid < 32) {  // the first of the two warps tells the others which item is next
-            if (n > 1 && !wait_bar(sm, &sm.frag_empty[n & 1], ((n >> 1) - 1) & 1)) return;
-            if (tid == 0) {
-                if (!more) f.rows = 0;
-                sm.frag[n & 1] = f;
-                mbar_arrive(&sm.frag_full[n & 1]);
-            }
-            __syncwarp();
+        if (n > 1 && !wait_bar(sm, &sm.frag_empty[n & 1], ((n >> 1) - 1) & 1)) return;
+        if (tid == 0) {  // tells the others which item is next
+            if (!more) f.rows = 0;
+            sm.frag[n & 1] = f;
+            mbar_arrive(&sm.frag_full[n & 1]);
         }
+        __syncwarp();
         if (!more) return;
         if (f.f1 == f.f0) continue;
         if (items > 0 && !wait_bar(sm, &sm.q_empty, (items - 1) & 1)) return;
-        const int row = tid >> 1;
-        if (row < R) {  // whole warps: R is 16 or 32
+#pragma unroll 1
+        for (int row = tid >> 1; row < R; row += 16) {
             const bool mine = row < f.rows;
             const int r = min(row, f.rows - 1), tok = r / g;
             const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q.p) + (int64_t)(f.s.row0 + tok) * a.q.ts +
                                   (int64_t)(f.h * g + r - tok * g) * a.q.hs + 8 * odd;
-            uint4 v[8];
+            constexpr int kCh = kDim / 16;
+            uint4 v[kCh];
             uint32_t top = 0;  // of the magnitudes' bits
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kCh; ++k) {
                 v[k] = mine ? *reinterpret_cast<const uint4*>(src + 16 * k) : make_uint4(0, 0, 0, 0);
                 top = max(top, top_bits(v[k]));
             }
@@ -329,7 +333,7 @@ __device__ void role_q(Smem<R>& sm, const KvAttn& a, int g, Cursor<R> cur) {
             const int e = big == 0.0f ? 0 : 7 - ((int)max(__float_as_uint(big) >> 23, 1u) - 127);
             const float f1 = pow2i(e / 2), f2 = pow2i(e - e / 2);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kCh; ++k) {
                 const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                 uint32_t out[3][2] = {};
 #pragma unroll
@@ -348,14 +352,14 @@ __device__ void role_q(Smem<R>& sm, const KvAttn& a, int g, Cursor<R> cur) {
                 }
 #pragma unroll
                 for (int s = 0; s < 3; ++s)  // channels 16 k + 8 odd ..
-                    *reinterpret_cast<uint2*>(&sm.q[sw128(s * R + row, k) + 8 * odd]) = make_uint2(out[s][0], out[s][1]);
+                    *reinterpret_cast<uint2*>(&sm.q[swizzled<kDim>(s * R + row, k) + 8 * odd]) = make_uint2(out[s][0], out[s][1]);
             }
             if (!odd) {
                 sm.c[items & 1][row] = times_pow2(c0, -e);
                 sm.pos[items & 1][row] = f.s.n - f.s.m + tok;
             }
-            fence_proxy_async_smem();
         }
+        fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_w(&sm.q_full);
         ++items;
@@ -407,8 +411,8 @@ __device__ __forceinline__ void load_terms(uint32_t taddr, float (&v)[R]) {
 
 // Waits that give up do not end the loops, so that a group's warps meet at the same
 // barriers; the results are not used then.
-template <int R, bool kBf>
-__device__ void role_softmax(Smem<R>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, uint32_t tb) {
+template <int kDim, int R, bool kBf>
+__device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g, uint32_t tb) {
     const int t = threadIdx.x >> 7, thr = threadIdx.x & 127, warp = thr >> 5, lane = threadIdx.x & 31;
     const uint32_t lane_base = tb + ((uint32_t)(32 * warp) << 16);
     const uint32_t ts = lane_base + kColS + 128 * t, to = lane_base + kColO + 128 * t;
@@ -509,7 +513,7 @@ __device__ void role_softmax(Smem<R>& sm, const KvAttn& a, const KvParts& parts,
                 }
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
-                    *reinterpret_cast<uint4*>(&sm.p[t][sw128(thr, (s * R + r0) >> 4)]) = make_uint4(out[s][0], out[s][1], out[s][2], out[s][3]);
+                    *reinterpret_cast<uint4*>(&sm.p[t][swizzled<128>(thr, (s * R + r0) >> 4)]) = make_uint4(out[s][0], out[s][1], out[s][2], out[s][3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -567,7 +571,7 @@ __device__ void role_softmax(Smem<R>& sm, const KvAttn& a, const KvParts& parts,
             int tok = 0, hd = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (r < f.rows) {
+                if (r < f.rows && thr < kDim) {
                     const float2 w = sm.join[r];
                     float v = nb > 0 ? o0[r] * w.x : 0.0f;
                     if (both) v = fmaf(o1[r], w.y, v);
@@ -591,21 +595,22 @@ __device__ void role_softmax(Smem<R>& sm, const KvAttn& a, const KvParts& parts,
     }
 }
 
-template <int R, bool kBf>
+template <int kDim, int R, bool kBf>
 __global__ void __launch_bounds__(kThreads, 1)
     k_kv_codes(const __grid_constant__ KvAttn a, const __grid_constant__ KvMaps maps, const __grid_constant__ KvPlan plan,
                const __grid_constant__ KvParts parts) {
     extern __shared__ uint8_t smem_raw[];
-    Smem<R>& sm = *reinterpret_cast<Smem<R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using S = Smem<kDim, R>;
+    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     static_assert(sizeof(KvPlanSmem) <= sizeof(sm.kv), "the plan's arrays lie in the ring");
-    static_assert(kRing > kPlaces / 2 + 4, "a block's mask is kept until its scores are read");
+    static_assert(kRing > S::kPlaces / 2 + 4, "a block's mask is kept until its scores are read");
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < kPlaces; ++i) {
+        for (int i = 0; i < S::kPlaces; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
-        mbar_init(&sm.q_full, 2);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
@@ -637,12 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   "more registers than the block was launched with");
     if (warp < 8) {
         if constexpr (R == 32) regs_up<kRegsSoftmax<R>>();
-        role_softmax<R, kBf>(sm, a, parts, per, plan.g, tb);
+        role_softmax<kDim, R, kBf>(sm, a, parts, per, plan.g, tb);
     } else {
         if constexpr (R == 32) regs_down<kRegsOther<R>>();
-        if (warp == kWarpMma) role_mma<R>(sm, tb);
-        else if (warp == kWarpTma) role_tma<R>(sm, a, maps, plan.g, cur);
-        else role_q<R, kBf>(sm, a, plan.g, cur);
+        if (warp == kWarpMma) role_mma<kDim, R>(sm, tb);
+        else if (warp == kWarpK) role_tma<kDim, R, false>(sm, a, maps, plan.g, cur);
+        else if (warp == kWarpV) role_tma<kDim, R, true>(sm, a, maps, plan.g, cur);
+        else role_q<kDim, R, kBf>(sm, a, plan.g, cur);
     }
     __syncwarp();
     __syncthreads();
@@ -659,15 +665,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int R, bool kBf>
+template <int kDim, int R, bool kBf>
 cudaError_t codes_as(const KvAttn& a, cudaStream_t st) {
-    constexpr int kSmem = sizeof(Smem<R>) + 1024;
+    constexpr int kSmem = sizeof(Smem<kDim, R>) + 1024;
     static_assert(kSmem <= 232448, "shared memory beyond the 227 KB per-block limit");
     KvMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
-    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kE4m3Bf16, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_pool_map(&maps.v, a.c.v, rows, kDim, kE4m3Bf16, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    constexpr CUtensorMapSwizzle kSwizzle = kDim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kE4m3Bf16, kDim, kSwizzle) ||
+        !make_pool_map(&maps.v, a.c.v, rows, kDim, kE4m3Bf16, kDim, kSwizzle))
         return cudaErrorInvalidValue;
     KvPlan plan;
     plan.g = a.H / a.c.kv_heads;
@@ -675,21 +682,26 @@ cudaError_t codes_as(const KvAttn& a, cudaStream_t st) {
     plan.min_per = kMinPer;
     const KvParts parts = kv_parts(a.ws, plan.grid, R, kDim);
     static std::atomic<uint64_t> attr_done{0};
-    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_codes<R, kBf>), kSmem, attr_done);
+    cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k_kv_codes<kDim, R, kBf>), kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    e = launch_behind(k_kv_codes<R, kBf>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
+    e = launch_behind(k_kv_codes<kDim, R, kBf>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
     if (e != cudaSuccess) return e;
     return launch_behind(k_kv_join<kDim, kBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts,
                          plan.g, R, plan.grid);
 }
 
+template <int kDim, int R>
+cudaError_t codes_type(const KvAttn& a, int dtype, cudaStream_t st) {
+    return dtype == CSA2_DTYPE_BF16 ? codes_as<kDim, R, true>(a, st) : codes_as<kDim, R, false>(a, st);
+}
+
 }  // namespace
 
-size_t kv_codes_workspace_bytes(bool few) { return kv_parts_bytes(device_sm_count(), few ? 16 : 32, kDim); }
+size_t kv_codes_workspace_bytes(bool few, int head_dim) { return kv_parts_bytes(device_sm_count(), few ? 16 : 32, head_dim); }
 
-cudaError_t launch_kv_codes(const KvAttn& a, bool few, int dtype, cudaStream_t st) {
-    if (dtype == CSA2_DTYPE_BF16) return few ? codes_as<16, true>(a, st) : codes_as<32, true>(a, st);
-    return few ? codes_as<16, false>(a, st) : codes_as<32, false>(a, st);
+cudaError_t launch_kv_codes(const KvAttn& a, bool few, int head_dim, int dtype, cudaStream_t st) {
+    if (head_dim == 64) return few ? codes_type<64, 16>(a, dtype, st) : codes_type<64, 32>(a, dtype, st);
+    return few ? codes_type<128, 16>(a, dtype, st) : codes_type<128, 32>(a, dtype, st);
 }
 
 }  // namespace csa2

@@ -11,19 +11,13 @@
 //   P = 2^(c S - m), kept in registers: the accumulators of S are P's operand
 //   O += P V    mma m16n8k16 (K = 16 keys)
 //
-// (mma.sync, not tcgen05: 16 rows of its 128 would be used, and the
-// operands come out of registers without a hand-over.)  An E4M3 cache (heads of 64;
-// kv_codes.cu takes those of 128) is widened
-// to fp16 in registers (exact): two bytes of a key's fragment are neighbouring
-// channels, so Q is read with its channels in the same order; two bytes of a
-// value's (transposed) fragment are two channels of one key, which byte
-// permutations pair by key.  Queries are scaled per row as in kv_mma.cu.
+// (mma.sync, not tcgen05: 16 rows of its 128 would be used, and the operands come
+// out of registers without a hand-over.)  Caches of 16 bits; kv_codes.cu takes E4M3.
 // The work is cut evenly over the CTAs (kv_plan.cuh), which splits long
 // sequences when there are few.
 //
 // One token of 16 sequences to 32,768, 64 / 8 heads of 128, bf16: 209 us (6.3 TB/s,
-// 98% of the copy rate); heads of 64: 83%, and 51% over E4M3 pages, where the
-// conversions and the byte permutations of half as many bytes take as long.
+// 98% of the copy rate); heads of 64: 83%.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -52,10 +46,8 @@ constexpr int kCtasPerSm = 2;
 
 template <int kDim, int kMode>
 struct __align__(1024) Smem {
-    static constexpr int kElem = is_e4m3(kMode) ? 1 : 2;
-    static constexpr int kRowBytes = kDim * kElem < 128 ? kDim * kElem : 128;  // of a slab
-    static constexpr int kSlabs = kDim * kElem / kRowBytes;
-    static constexpr int kPageBytes = PAGE * kDim * kElem;
+    static constexpr int kSlabs = kDim / 64;  // of 128-byte rows
+    static constexpr int kPageBytes = PAGE * kDim * 2;
     static constexpr int kQStride = kDim * 2 + 16;
     static constexpr int kRedBytes = 2 * kRows * kDim * 4;  // two warps' sums
     static constexpr int kRoom = 112 * 1024 - kRedBytes - kRows * kQStride - 2048;
@@ -64,7 +56,6 @@ struct __align__(1024) Smem {
     uint8_t q[kRows][kQStride];
     float red[2][kRows][kDim];
     float ml[kWarps][kRows][2];
-    float qc[kRows];
     uint8_t bad[kStages];
     uint64_t full[kStages], empty[kStages];
     int abort;
@@ -89,11 +80,9 @@ __device__ __forceinline__ bool wait_bar_warp(S& sm, uint64_t* bar, uint32_t par
 }
 
 // Byte offset of 16-byte chunk c (of the whole row) of a page's row r: slabs of
-// 128-byte rows with the 128-byte swizzle, or 64-byte rows with the 64-byte one.
-template <class S>
+// 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t at16(int r, int c) {
-    if constexpr (S::kRowBytes == 128) return (c >> 3) * (PAGE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return (c >> 3) * (PAGE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -153,8 +142,8 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& 
 #pragma unroll
                 for (int i = 0; i < 2 * S::kSlabs; ++i) {
                     const int v = i / S::kSlabs, c = i % S::kSlabs;
-                    tma_load_2d_nohint_w(&sm.kv[st][v][c * PAGE * S::kRowBytes], v ? &maps.v : &maps.k,
-                                         c * (S::kRowBytes / S::kElem), (id * a.c.kv_heads + f.h) * PAGE, &sm.full[st]);
+                    tma_load_2d_nohint_w(&sm.kv[st][v][c * PAGE * 128], v ? &maps.v : &maps.k,
+                                         64 * c, (id * a.c.kv_heads + f.h) * PAGE, &sm.full[st]);
                 }
             }
             __syncwarp();
@@ -175,8 +164,7 @@ template <int kDim, int kMode>
 __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g,
                           Cursor cur) {
     using S = Smem<kDim, kMode>;
-    constexpr bool kBf = kMode == kBf16;                           // operands
-    constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;  // q and out
+    constexpr bool kBf = kMode == kBf16;
     constexpr int kKs = kDim / 16, kNt = kDim / 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, qc = lane & 3;
     const float c0 = fmaxf(a.scale * kLog2e, FLT_MIN);
@@ -197,36 +185,19 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                                                         (int64_t)(f.s.row0 + t) * a.q.ts +
                                                         (int64_t)(f.h * g + r - t * g) * a.q.hs + 8 * c);
                 }
-                if constexpr (kMode == kE4m3Bf16) {
-                    uint32_t top = top_bits(v);  // the row's chunks are neighbouring lanes'
-#pragma unroll
-                    for (int d = kCh / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    v = scaled(v, row_exp(top));
-                    if (c == 0) sm.qc[r] = times_pow2(c0, -row_exp(top));
-                }
                 *reinterpret_cast<uint4*>(&sm.q[r][16 * c]) = v;
             }
             warps_sync();
         }
         uint32_t qf[kKs][4];
-        auto load_q = [&](int ks, uint32_t (&r)[4]) {
-            if constexpr (is_e4m3(kMode)) {  // channels 4 c .. 4 c + 3 of the 16
-                const uint2 x = *reinterpret_cast<const uint2*>(&sm.q[quad][32 * ks + 8 * qc]);
-                const uint2 y = *reinterpret_cast<const uint2*>(&sm.q[quad + 8][32 * ks + 8 * qc]);
-                r[0] = x.x, r[1] = y.x, r[2] = x.y, r[3] = y.y;
-            } else {
-                ldsm4(smem_u32(&sm.q[lane & 15][32 * ks + 16 * (lane >> 4)]), r);
-            }
-        };
         int pos[2], lo[2];
-        float cc[2], mref[2], l[2];
+        float mref[2], l[2];
         float o[kNt][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = min(quad + 8 * e, f.rows - 1);
             pos[e] = f.s.n - f.s.m + r / g;
             lo[e] = a.window > 0 ? max(0, pos[e] - a.window + 1) : 0;
-            cc[e] = kMode == kE4m3Bf16 && nb > 0 ? sm.qc[quad + 8 * e] : c0;
             mref[e] = -INFINITY, l[e] = 0.0f;
         }
         const int pos_min = f.s.n - f.s.m, lo_max = a.window > 0 ? max(0, f.v.hi - a.window + 1) : 0;
@@ -236,7 +207,7 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
             for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
         if (nb > 0) {
 #pragma unroll
-            for (int ks = 0; ks < kKs; ++ks) load_q(ks, qf[ks]);
+            for (int ks = 0; ks < kKs; ++ks) ldsm4(smem_u32(&sm.q[lane & 15][32 * ks + 16 * (lane >> 4)]), qf[ks]);
         }
         for (int j = f.f0; j < f.f1; ++j) {
             // a wait that gave up does not end the loop: the warps meet at the same barriers
@@ -246,10 +217,10 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                 const uint32_t kp = smem_u32(sm.kv[st][0]), vp = smem_u32(sm.kv[st][1]);
                 const bool edge = kb + 15 > f.v.hi || kb < f.v.lo;
                 if (edge) {  // rows of V that no query sees: zero, as 0 x NaN is not
-                    for (int i = lane; i < 16 * (kDim * S::kElem / 16); i += 32) {
+                    for (int i = lane; i < 16 * (kDim / 8); i += 32) {
                         const int r = i & 15, key = kb + r;
                         if (key > f.v.hi || key < f.v.lo)
-                            *reinterpret_cast<uint4*>(sm.kv[st][1] + at16<S>(16 * warp + r, i >> 4)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(sm.kv[st][1] + at16(16 * warp + r, i >> 4)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();  // the stage is next written by a TMA
                     __syncwarp();
@@ -261,28 +232,12 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
                 const int kr = 16 * warp + (lane & 7) + ((lane >> 4) << 3);  // ldmatrix row of this lane
-                if constexpr (!is_e4m3(kMode)) {
 #pragma unroll
-                    for (int ks = 0; ks < kKs; ++ks) {
-                        uint32_t b[4];
-                        ldsm4(kp + at16<S>(kr, 2 * ks + ((lane >> 3) & 1)), b);
-                        mma16816<kBf>(s[0], qf[ks], b[0], b[1]);
-                        mma16816<kBf>(s[1], qf[ks], b[2], b[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int ks = 0; ks < kKs; ks += 2) {
-                        uint32_t b[4];  // (keys 0-7, 16 channels), (keys 0-7, next 16), (keys 8-15, ..)
-                        ldsm4(kp + at16<S>(kr, ks + ((lane >> 3) & 1)), b);
-#pragma unroll
-                        for (int k2 = 0; k2 < 2; ++k2) {
-                            uint32_t w[4];
-                            e4m3x4_to_h2(b[k2], w[0], w[1]);
-                            e4m3x4_to_h2(b[2 + k2], w[2], w[3]);
-                            mma16816<false>(s[0], qf[ks + k2], w[0], w[1]);
-                            mma16816<false>(s[1], qf[ks + k2], w[2], w[3]);
-                        }
-                    }
+                for (int ks = 0; ks < kKs; ++ks) {
+                    uint32_t b[4];
+                    ldsm4(kp + at16(kr, 2 * ks + ((lane >> 3) & 1)), b);
+                    mma16816<kBf>(s[0], qf[ks], b[0], b[1]);
+                    mma16816<kBf>(s[1], qf[ks], b[2], b[3]);
                 }
                 // ---- softmax: elements 0, 1 of row quad, 2, 3 of row quad + 8
                 if (kb + 15 > pos_min || kb < lo_max) {
@@ -301,7 +256,7 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                     float x = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    bm[e] = x * cc[e];
+                    bm[e] = x * c0;
                     move = move || bm[e] > mref[e] + kGap || (mref[e] == -INFINITY && bm[e] > -INFINITY);
                 }
                 if (__any_sync(0xffffffffu, move)) {
@@ -321,36 +276,19 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float ms = mref[e] == -INFINITY ? 0.0f : mref[e];
-                        const float x = ex2(fmaf(s[t][2 * e], cc[e], -ms));
-                        const float y = ex2(fmaf(s[t][2 * e + 1], cc[e], -ms));
+                        const float x = ex2(fmaf(s[t][2 * e], c0, -ms));
+                        const float y = ex2(fmaf(s[t][2 * e + 1], c0, -ms));
                         l[e] += x + y;
                         p[2 * t + e] = pack16(x, y, kBf);
                     }
                 // ---- O
                 const int vr = 16 * warp + (lane & 15);
-                if constexpr (!is_e4m3(kMode)) {
 #pragma unroll
-                    for (int t = 0; t < kNt; t += 2) {
-                        uint32_t b[4];  // (keys 0-7, 8 channels), (keys 8-15, ..), the next 8 channels
-                        ldsm4t(vp + at16<S>(vr, t + (lane >> 4)), b);
-                        mma16816<kBf>(o[t], p, b[0], b[1]);
-                        mma16816<kBf>(o[t + 1], p, b[2], b[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < kNt; t += 4) {
-                        uint32_t b[4];  // (keys 0-7, 16 channels), (keys 8-15, ..), the next 16 channels
-                        ldsm4t(vp + at16<S>(vr, t / 2 + (lane >> 4)), b);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            // even channels: bytes 0, 2 (keys 2 c, 2 c + 1); odd ones: bytes 1, 3
-                            uint32_t e0, e1, d0, d1;
-                            e4m3x4_to_h2(__byte_perm(b[2 * u], 0, 0x3120), e0, d0);
-                            e4m3x4_to_h2(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, d1);
-                            mma16816<false>(o[t + 2 * u], p, e0, e1);
-                            mma16816<false>(o[t + 2 * u + 1], p, d0, d1);
-                        }
-                    }
+                for (int t = 0; t < kNt; t += 2) {
+                    uint32_t b[4];  // (keys 0-7, 8 channels), (keys 8-15, ..), the next 8 channels
+                    ldsm4t(vp + at16(vr, t + (lane >> 4)), b);
+                    mma16816<kBf>(o[t], p, b[0], b[1]);
+                    mma16816<kBf>(o[t + 1], p, b[2], b[3]);
                 }
             }
             __syncwarp();
@@ -375,31 +313,18 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
             const float M = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
             w[e] = M == -INFINITY ? 1.0f : ex2(mref[e] - M);  // no key seen: zeros, or NaN scores' NaN
         }
-        // channel of element e of accumulator t: neighbouring pairs, but for E4M3 every other one
         auto place = [&](bool add, int buf) {
 #pragma unroll
-            for (int t = 0; t < kNt; t += is_e4m3(kMode) ? 2 : 1)
+            for (int t = 0; t < kNt; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float* row = sm.red[buf][quad + 8 * e];
-                    if constexpr (is_e4m3(kMode)) {
-                        float4* d = reinterpret_cast<float4*>(row + 8 * t + 4 * qc);
-                        float4 v = make_float4(o[t][2 * e], o[t + 1][2 * e], o[t][2 * e + 1], o[t + 1][2 * e + 1]);
-                        v.x *= w[e], v.y *= w[e], v.z *= w[e], v.w *= w[e];
-                        if (add) {
-                            const float4 u = *d;
-                            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-                        }
-                        *d = v;
-                    } else {
-                        float2* d = reinterpret_cast<float2*>(row + 8 * t + 2 * qc);
-                        float2 v = make_float2(o[t][2 * e] * w[e], o[t][2 * e + 1] * w[e]);
-                        if (add) {
-                            const float2 u = *d;
-                            v.x += u.x, v.y += u.y;
-                        }
-                        *d = v;
+                    float2* d = reinterpret_cast<float2*>(&sm.red[buf][quad + 8 * e][8 * t + 2 * qc]);
+                    float2 v = make_float2(o[t][2 * e] * w[e], o[t][2 * e + 1] * w[e]);
+                    if (add) {
+                        const float2 u = *d;
+                        v.x += u.x, v.y += u.y;
                     }
+                    *d = v;
                 }
         };
         if (warp < 2) place(false, warp);
@@ -430,7 +355,7 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                 const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                 uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = L == 0.0f ? 0u : pack16(v[2 * e] * inv, v[2 * e + 1] * inv, kOutBf);
+                for (int e = 0; e < 4; ++e) u[e] = L == 0.0f ? 0u : pack16(v[2 * e] * inv, v[2 * e + 1] * inv, kBf);
                 *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out.p) + token * a.out.ts + (int64_t)head * a.out.hs +
                                           8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
                 if (a.lse && c == 0) a.lse[token * a.H + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -486,9 +411,8 @@ cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
     KvMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t rows = (int64_t)a.c.num_pages * a.c.kv_heads * PAGE;
-    constexpr CUtensorMapSwizzle swizzle = S::kRowBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode, S::kRowBytes, swizzle) ||
-        !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode, S::kRowBytes, swizzle))
+    if (!make_pool_map(&maps.k, a.c.k, rows, kDim, kMode, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_pool_map(&maps.v, a.c.v, rows, kDim, kMode, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     KvPlan plan;
     plan.g = a.H / a.c.kv_heads;
@@ -500,8 +424,8 @@ cudaError_t rows_as(const KvAttn& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_behind(k_kv_rows<kDim, kMode>, dim3(plan.grid), kThreads, kSmem, st, a, maps, plan, parts);
     if (e != cudaSuccess) return e;
-    constexpr bool kOutBf = kMode == kBf16 || kMode == kE4m3Bf16;
-    return launch_behind(k_kv_join<kDim, kOutBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, kRows, plan.grid);
+    constexpr bool kBf = kMode == kBf16;
+    return launch_behind(k_kv_join<kDim, kBf, false>, dim3(kJoinBlocksPerSm * device_sm_count()), kJoinThreads, 0, st, a, parts, plan.g, kRows, plan.grid);
 }
 
 }  // namespace
@@ -510,13 +434,8 @@ size_t kv_rows_workspace_bytes(int head_dim) {
     return kv_parts_bytes(kCtasPerSm * device_sm_count(), kRows, head_dim);
 }
 
-// E4M3 pages: heads of 64 (kv_codes.cu takes those of 128).
-cudaError_t launch_kv_rows(const KvAttn& a, int head_dim, int dtype, int kv_dtype, cudaStream_t st) {
+cudaError_t launch_kv_rows(const KvAttn& a, int head_dim, int dtype, cudaStream_t st) {
     const bool bf = dtype == CSA2_DTYPE_BF16;
-    if (kv_dtype == CSA2_KV_E4M3) {
-        if (head_dim != 64) return cudaErrorInvalidValue;
-        return bf ? rows_as<64, kE4m3Bf16>(a, st) : rows_as<64, kE4m3F16>(a, st);
-    }
     if (head_dim == 64) return bf ? rows_as<64, kBf16>(a, st) : rows_as<64, kF16>(a, st);
     return bf ? rows_as<128, kBf16>(a, st) : rows_as<128, kF16>(a, st);
 }
