@@ -17,8 +17,9 @@
 //
 // 4,096 tokens of 64 heads of 512, the last 64 rotating, bf16: 92 us (5.9 TB/s, 91% of
 // the copy rate).  8,191 tokens of 16 heads of 128, three axes, fp16: 15 us (70%; issue
-// slots 67% busy).  Append of 16 x 8,192 tokens, 8 heads of 128, to E4M3 pages: 174 us
-// (4.6 TB/s, 72%; issue slots 63% busy with angles and conversions).
+// slots 67% busy).  Append of 16 x 8,192 tokens, 8 heads of 128, to E4M3 pages: 170 us
+// (4.7 TB/s, 73%; issue slots 63% busy; a cheaper sine and cosine, packed products and
+// other tile sizes changed nothing).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -27,7 +28,7 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (256 and 512: 3% and 18% slower for the large append)
 template <typename In>
 constexpr int kUnits = sizeof(In) == 4 ? 2 : 4;  // units of a thread
 
