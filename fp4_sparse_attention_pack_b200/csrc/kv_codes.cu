@@ -12,13 +12,16 @@
 // where x1 = rn(x), x2 = rn(2^4 (x - x1)), x3 = rn(2^4 (2^4 (x - x1) - x2)); R is 16 or
 // 32.  A row's queries are scaled by a power of two that takes the largest into
 // [2^7, 2^8), undone in the softmax scale; terms are exact to 2^-27 of it.
-// Probabilities are rounded to fp16 first and then split exactly (down to 2^-18).
+// Probabilities are rounded to fp16 first and then split.  The reference of a row's
+// exponentials is its maximum less 4 (log2) when it is taken, and moves when a score
+// exceeds it by more than 8: the largest probability lies in [2^4, 2^8], E4M3's range,
+// and the third term's rounding, 2^-18, is at most 2^-22 of it.  (Less 5 or 6 would
+// move it more often: 4 and 20% longer with 32 rows.)
 //
 // One CTA an SM, 384 threads, blocks of 128 keys:
 //   warps 0-3, 4-7  softmax of even and odd blocks, each with sums and a maximum of
 //                   its own: thread = key (TMEM lane of S^T); at an item's end thread
-//                   = channel (lane of O^T).  The maxima in use move only when a score
-//                   exceeds one by more than 8 (log2).
+//                   = channel (lane of O^T);
 //   warp 8          issues the MMAs;
 //   warps 9, 11     load pages by TMA, K and V (one warp for both took 1,600 cycles a
 //                   block, more than the bytes);
@@ -26,7 +29,7 @@
 //
 // The cache's bytes bound it: one token of 8 sequences over 65,536, 64 / 8 heads of
 // 128, takes 176 us (6.1 TB/s, 94% of the copy rate); with 32 rows (4 tokens each) the
-// softmax warps' instructions, some 470 a thread and block, bring it to 215 us (77%),
+// softmax warps' instructions, some 470 a thread and block, bring it to 215 us (78%),
 // and heads of 64, whose blocks have half the bytes, to 130 and 193 us (64%, 43%).
 #include <algorithm>
 #include <atomic>
@@ -57,7 +60,8 @@ constexpr int kWarpMma = 8, kWarpK = 9, kWarpQ = 10, kWarpV = 11;
 constexpr int places_of(int dim) { return dim == 64 ? 16 : 10; }  // K and V blocks in the order of their use
 constexpr int kRing = 16;    // blocks whose masks of bad pages are kept
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // two of each, 128 columns apart
-constexpr float kNone = -FLT_MAX / 2;                         // maximum in use before any
+constexpr float kNone = -FLT_MAX / 2;                         // reference before any score
+constexpr float kBelow = 4.0f;                                // by which a reference is below the maximum
 
 template <int kDim, int R>
 struct Smem {
@@ -65,10 +69,10 @@ struct Smem {
     alignas(16) uint8_t kv[kPlaces][kBlk * kDim];  // [key][channel], swizzled by its width
     uint8_t p[2][kBlk * 128];                     // [key][3 R codes], SW128
     uint8_t q[3 * R * kDim];                      // [term][row][channel], as kv
-    float4 cm[2][R / 2];                          // (c, -maximum) of two rows each
+    float4 cm[2][R / 2];                          // (c, -reference) of two rows each
     float factor[2][R];
     float wmax[2][4][32], wsum[2][4][32];
-    float2 pair[R];                               // odd blocks' (maximum, sum)
+    float2 pair[R];                               // odd blocks' (reference, sum)
     float2 join[R];                               // weights of even and odd blocks' sums
     float c[2][R];                                // softmax scale of each row (per item parity)
     int pos[2][R];                                // its last key
@@ -472,7 +476,7 @@ __device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& 
                 group_sync(t);
                 const float2 cm = reinterpret_cast<const float2*>(sm.cm[t])[row];
                 const float most = fmaxf(fmaxf(sm.wmax[t][0][row], sm.wmax[t][1][row]), fmaxf(sm.wmax[t][2][row], sm.wmax[t][3][row])) * cm.x;
-                const float old = -cm.y, now = most > old + kGap ? most : old;
+                const float old = -cm.y, now = most > old + kGap ? most - kBelow : old;
                 group_sync(t);
                 if (warp == 0 && lane < R) {
                     sm.factor[t][lane] = ex2(old - now);

@@ -27,10 +27,10 @@ def make(csa, old, new, H, hk, dim, dtype, cache, **kw):
 
 
 def plain(c, scale, window=0):
-    """The definition in fp64 on the GPU: (out, lse, sum of p |v|), rows of all sequences."""
+    """The definition in fp64 on the GPU: (out, lse, sum of p |v|, sum of |v| that is seen), rows of all sequences."""
     g, n_tok = c.H // c.kv_heads, c.n_tokens.tolist()
     out = torch.zeros(c.used, c.H, c.dim, dtype=torch.float64, device="cuda")
-    mag, lse = torch.zeros_like(out), torch.zeros(c.used, c.H, dtype=torch.float64, device="cuda")
+    mag, vsum, lse = torch.zeros_like(out), torch.zeros_like(out), torch.zeros(c.used, c.H, dtype=torch.float64, device="cuda")
     row = 0
     for b, m in enumerate(c.new):
         n = n_tok[b]
@@ -47,19 +47,24 @@ def plain(c, scale, window=0):
             p = torch.softmax(s, -1)
             out[row:row + m, h * g:(h + 1) * g] = p @ v[:, h]
             mag[row:row + m, h * g:(h + 1) * g] = p @ v[:, h].abs()
+            vsum[row:row + m, h * g:(h + 1) * g] = (seen.double() @ v[:, h].abs())[:, None]
             lse[row:row + m, h * g:(h + 1) * g] = torch.logsumexp(s, -1)
         row += m
-    return out, lse, mag
+    return out, lse, mag, vsum
 
 
 def close(c, got, lse, scale, window=0, s_max=64.0):
     """u_p is the rounding of the probabilities; scores are below s_max, so fp32 products of `dim` terms, their sums and
-    exp2 leave at most 2 s_max dim 2^-24 in the exponent; the polynomial of a quarter of them 2^-18."""
-    want, l, mag = plain(c, scale, window)
+    exp2 leave at most 2 s_max dim 2^-24 in the exponent; the polynomial of a quarter of them 2^-18.  A probability of
+    fp16 is a multiple of 2^-24 with a row's largest at 1 or more, one of three E4M3 terms a multiple of 2^-17 with the
+    largest at 2^4 or more, so each is off by up to half of that on top: 2^-25 or 2^-22 of the largest, which is no more
+    than their sum."""
+    want, l, mag, vsum = plain(c, scale, window)
     eps = 2 * s_max * c.dim * 2.0 ** -24 + 2.0 ** -18
     u_p = 2.0 ** -8 if c.cache_dtype == BF else 2.0 ** -11
     u_o = 2.0 ** -8 if c.dtype == BF else 2.0 ** -11
-    bound = (u_p + eps) * mag + u_o * (want.abs() + (u_p + eps) * mag) + 2.0 ** -25
+    p_err = (u_p + eps) * mag + {BF: 0.0, HF: 2.0 ** -25, E4: 2.0 ** -22}[c.cache_dtype] * vsum
+    bound = p_err + u_o * (want.abs() + p_err) + 2.0 ** -25
     d = (got[:c.used].double() - want).abs()
     assert (d <= bound).all(), (d - bound).max()
     assert ((lse[:c.used].double() - l).abs() <= eps + 2.0 ** -23 * l.abs()).all()
@@ -222,3 +227,24 @@ def test_tensors_that_are_refused(csa):
             csa.kv_append(**{**dict(cache=c.desc, k=k, v=k, cu=c.cu, max_new=2), **kw})
     torch.cuda.synchronize()
     assert c.status[0].item() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("old,new,H,hk,window", [
+    ([9000, 100, 5, 63, 0], [4, 3, 0, 2, 4], 8, 1, 0),     # 32 rows, a long sequence over many CTAs
+    ([127, 128, 255, 256, 383, 0], [1] * 6, 20, 1, 0),     # 20 rows, one to four blocks
+    ([124, 252, 60], [4, 4, 4], 16, 2, 0),                 # the new tokens end a page, a block
+    ([3000, 500, 90], [3, 2, 1], 20, 2, 100),              # 30 rows through a window
+    ([700, 64], [2, 1], 16, 2, 0),                         # 16 rows
+    ([5000, 1], [1, 1], 5, 1, 64),
+])
+def test_codes_read_by_the_tensor_cores(csa, dtype, dim, old, new, H, hk, window):
+    """E4M3 pages with at most 32 rows to a kv head."""
+    c = make(csa, old, new, H, hk, dim, dtype, E4, seed=H + dim)
+    c.hold_all()
+    for scale in (dim ** -0.5, 1.0):  # the second: scores to +-50, one key takes nearly all
+        out, lse = c.attend(scale, window)
+        torch.cuda.synchronize()
+        assert c.status[0].item() == 0
+        close(c, out, lse, scale, window, s_max=128.0)
