@@ -290,10 +290,12 @@ __device__ void role_tma(Smem<kDim, R>& sm, const KvAttn& a, const KvMaps& maps,
         base += 2 * nb;
         blocks += nb;
     }
-    // no copy is in flight when the CTA ends, also after a wait that gave up
+    // No copy is in flight when the CTA ends, also after a wait that gave up.  One limit
+    // for all: a place that the other warp has filled since may never show its parity.
     if (*reinterpret_cast<volatile int*>(&sm.abort)) {
+        const uint64_t t0 = global_ns();
         for (int p = 0; p < kPlaces; ++p)
-            if (issued >> p & 1) (void)mbar_wait(&sm.full[p], parity >> p & 1);
+            while (issued >> p & 1 && !mbar_try(&sm.full[p], parity >> p & 1) && global_ns() - t0 < kWaitNs);
     }
 }
 
