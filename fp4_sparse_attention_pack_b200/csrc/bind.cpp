@@ -81,6 +81,8 @@ csa2_heads heads(const at::Tensor& t, const char* what, std::initializer_list<in
         s << what << " must be " << type << " of shape " << text(shape) << ", not " << text(t);
         refuse(s.str());
     }
+    for (int i = 0; i < 3; ++i)
+        if (t.size(i) != (int)t.size(i)) refuse(std::string(what) + " of " + text(t.sizes()) + ": sizes are counted in 32 bits");
     if (t.size(2) > 1 && t.stride(2) != 1) refuse(std::string(what) + ": the channels must be contiguous");
     return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
 }

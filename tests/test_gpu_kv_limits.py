@@ -229,6 +229,22 @@ def test_tensors_that_are_refused(csa):
     assert c.status[0].item() == 0
 
 
+def test_sizes_beyond_32_bits_are_refused(csa):
+    """Broadcast tensors can have them without the memory; nothing is written."""
+    c = make(csa, [10], [1], 4, 2, 64, BF, BF)
+    k, cu = torch.ones(1, 2, 64, dtype=BF, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    before, count = c.k_pages.clone(), c.n_tokens.clone()
+    many = k.expand((1 << 32) + 1, 2, 64)
+    with pytest.raises(ValueError):
+        csa.kv_append(c.desc, many, many, cu, 1)
+    x = torch.ones(1, 1, 64, dtype=BF, device="cuda")
+    wide = x.expand(1, (1 << 32) + 1, 64)
+    with pytest.raises(ValueError):
+        csa.rotate(csa.rotary(torch.ones(16, device="cuda"), 32), wide, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), wide)
+    torch.cuda.synchronize()
+    assert torch.equal(c.k_pages.view(torch.int16), before.view(torch.int16)) and torch.equal(c.n_tokens, count)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("old,new,H,hk,window", [
