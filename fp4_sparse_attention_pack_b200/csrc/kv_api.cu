@@ -178,7 +178,7 @@ int csa2_kv_attn(const csa2_kv_cache* cache, const csa2_heads* q, int H, int dty
     a.H = H;
     a.total = total;
     a.max_new = max_new;
-    a.window = window;
+    a.window = window < cache->max_pages * PAGE ? window : 0;  // one of the whole capacity hides nothing
     a.scale = scale;
     return cuda_status(launch_kv_attn(a, cache->head_dim, dtype, cache->dtype, (cudaStream_t)stream));
 }

@@ -433,7 +433,7 @@ __device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& 
         if (nb > 0) ++items;
         blocks += nb;
         const int pos_min = f.s.n - f.s.m, window = a.window;
-        const int lo_max = window > 0 ? max(0, f.v.hi - window + 1) : 0;
+        const int lo_max = first_key(f.v.hi, window);
         float l[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = 0.0f;
@@ -454,7 +454,7 @@ __device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& 
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int p = sm.pos[it][r];
-                    if (gone || key > p || (window > 0 && key <= p - window)) x[r] = -INFINITY;
+                    if (gone || key > p || (window > 0 && key <= p - window)) x[r] = -INFINITY;  // p >= -32
                 }
             }
             float y[R], top = -INFINITY;

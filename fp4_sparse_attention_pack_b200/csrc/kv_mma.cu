@@ -558,7 +558,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
             {
                 const int x = f.tile * kTile - f.v.t0 * g + min(ri, f.rows - 1);
                 pos = f.s.n - f.s.m + f.v.t0 + x / g;
-                lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                lo = first_key(pos, a.window);
             }
             float mref = -INFINITY, l = 0.0f;
             float c = fmaxf(a.scale * kLog2e, FLT_MIN);  // never 0: a masked score is -infinity

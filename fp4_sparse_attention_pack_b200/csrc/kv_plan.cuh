@@ -36,6 +36,13 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttn& a, int b) {
     return {t.row0, t.m, kv_held(a.c, b)};
 }
 
+// The first key that a row at position `pos` sees.  A position may lie 2^31 - 4096 below
+// 0 (more new tokens than the cache holds), so the window is subtracted only where it
+// begins behind key 0.
+__device__ __forceinline__ int first_key(int pos, int window) {
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // The keys [lo, hi] and blocks [b0, b1) that the rows of a tile see.
 struct KvSpan {
     int t0, lo, hi, b0, b1;
@@ -46,7 +53,7 @@ __device__ __forceinline__ KvSpan kv_span(const KvSeq& s, int g, int window, int
     KvSpan v;
     v.t0 = tile * kTile / g;
     v.hi = s.n - s.m + r1 / g;
-    v.lo = window > 0 ? max(0, s.n - s.m + v.t0 - window + 1) : 0;
+    v.lo = first_key(s.n - s.m + v.t0, window);
     v.b0 = v.lo / kBlk;
     v.b1 = v.hi < 0 ? v.b0 : v.hi / kBlk + 1;
     return v;

@@ -197,10 +197,10 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
         for (int e = 0; e < 2; ++e) {
             const int r = min(quad + 8 * e, f.rows - 1);
             pos[e] = f.s.n - f.s.m + r / g;
-            lo[e] = a.window > 0 ? max(0, pos[e] - a.window + 1) : 0;
+            lo[e] = first_key(pos[e], a.window);
             mref[e] = -INFINITY, l[e] = 0.0f;
         }
-        const int pos_min = f.s.n - f.s.m, lo_max = a.window > 0 ? max(0, f.v.hi - a.window + 1) : 0;
+        const int pos_min = f.s.n - f.s.m, lo_max = first_key(f.v.hi, a.window);
 #pragma unroll
         for (int t = 0; t < kNt; ++t)
 #pragma unroll
