@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 128;  // (256 and 512: 3% and 18% slower for the large append)
 template <typename In>
 constexpr int kUnits = sizeof(In) == 4 ? 2 : 4;  // units of a thread
+constexpr int kMaxTokens = 64;                   // of a CTA
 
 template <typename T>
 struct Vec8;  // 8 channels as they lie in memory
@@ -328,6 +329,43 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
     const int h0 = blockIdx.y * ht, nh = min(ht, a.c.kv_heads - h0);
     const int total = nt * nh * (int)(kinds.turn.d + kinds.other.d + kinds.value.d);
     const Divisor per_token = divisor(nh);
+    const auto load = [&](Unit<In>& v, const Where& w) {
+        const HeadsView& x = w.kind() == 2 ? a.v : a.k;
+        const In* src = reinterpret_cast<const In*>(x.p) + (int64_t)(t0 + w.t()) * x.ts + (h0 + w.h()) * x.hs;
+        if (w.kind() == 0) load_turn(v, src, w.u(), r);
+        else if (w.kind() == 1) load_plain(v, src + other_channel(r, w.u(), kinds.width), kinds.width);
+        else load_plain(v, src + 16 * w.u(), 16);
+    };
+    const auto store = [&](const Unit<In>& v, const Where& w) {
+        const int64_t at = row[w.t()];
+        if (at < 0) return;
+        Out* dst = reinterpret_cast<Out*>(w.kind() == 2 ? a.c.v : a.c.k) + at + (int64_t)(h0 + w.h()) * PAGE * dim;
+        if (w.kind() == 0) store_turn(v, dst, w.u(), r, cs + w.t() * half);
+        else if (w.kind() == 1) store_plain(v, dst + other_channel(r, w.u(), kinds.width), kinds.width);
+        else store_plain(v, dst + 16 * w.u(), 16);
+    };
+    // Where token threadIdx.x goes if it belongs to sequence b.
+    const auto locate = [&](int b) {
+        const int t = t0 + threadIdx.x;
+        int64_t at = -1;
+        int s = 0;
+        const Placed p = place(a, cu, b);
+        if (p.m > 0 && t >= p.row0 && t < p.row0 + p.m) {
+            s = p.slot0 + (t - p.row0);
+            const int page = kv_page(a.c, b, s / PAGE);
+            if (page >= 0) at = ((int64_t)page * a.c.kv_heads * PAGE + s % PAGE) * dim;
+        }
+        row[threadIdx.x] = at;
+        slot[threadIdx.x] = s;
+    };
+    const auto turns = [&] {
+        for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+            const int t = divide(i, pairs), p = i - t * half;
+            if (row[t] >= 0)
+                cs[t * half + cs_at(r, p)] = turn_of(r, p, r.pos ? r.pos[axis_of(r, p) * r.pos_stride + t0 + t] : slot[t]);
+        }
+    };
+    static_assert(kMaxTokens <= kThreads, "a thread looks up one token");
     Unit<In> v[kUnits<In>];
     Where w[kUnits<In>];
 #pragma unroll
@@ -335,50 +373,48 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
         const int i = threadIdx.x + k * kThreads;
         if (i >= total) continue;
         w[k] = where(i, nt, nh, per_token, kinds);
-        const HeadsView& x = w[k].kind() == 2 ? a.v : a.k;
-        const In* src = reinterpret_cast<const In*>(x.p) + (int64_t)(t0 + w[k].t()) * x.ts + (h0 + w[k].h()) * x.hs;
-        if (w[k].kind() == 0) load_turn(v[k], src, w[k].u(), r);
-        else if (w[k].kind() == 1) load_plain(v[k], src + other_channel(r, w[k].u(), kinds.width), kinds.width);
-        else load_plain(v[k], src + 16 * w[k].u(), 16);
+        load(v[k], w[k]);
     }
-    for (int i = threadIdx.x; i <= a.c.batch; i += kThreads) cu[i] = a.cu[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt; i += kThreads) {
-        const int t = t0 + i;
-        int lo = 0, hi = a.c.batch;  // the last b with cu[b] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t) lo = mid;
-            else hi = mid;
+    bool ordered = true;
+    for (int i = threadIdx.x; i <= a.c.batch; i += kThreads) {
+        cu[i] = a.cu[i];
+        if (i < a.c.batch) ordered = ordered && cu[i] <= a.cu[i + 1];
+    }
+    ordered = __syncthreads_and(ordered);
+    if (ordered) {
+        if (threadIdx.x < nt) {
+            int lo = 0, hi = a.c.batch;  // the last b with cu[b] <= t: no other sequence has the row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t0 + (int)threadIdx.x) lo = mid;
+                else hi = mid;
+            }
+            locate(lo);
         }
-        const Placed p = place(a, cu, lo);
-        int64_t at = -1;
-        int s = 0;
-        if (p.m > 0 && t >= p.row0 && t < p.row0 + p.m) {
-            s = p.slot0 + (t - p.row0);
-            const int page = kv_page(a.c, lo, s / PAGE);
-            if (page >= 0) at = ((int64_t)page * a.c.kv_heads * PAGE + s % PAGE) * dim;
-        }
-        row[i] = at;
-        slot[i] = s;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = divide(i, pairs), p = i - t * half;
-        if (row[t] >= 0)
-            cs[t * half + cs_at(r, p)] = turn_of(r, p, r.pos ? r.pos[axis_of(r, p) * r.pos_stride + t0 + t] : slot[t]);
-    }
-    __syncthreads();
+        __syncthreads();
+        turns();
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kUnits<In>; ++k) {
-        const int i = threadIdx.x + k * kThreads;
-        if (i >= total) continue;
-        const int64_t at = row[w[k].t()];
-        if (at < 0) continue;
-        Out* dst = reinterpret_cast<Out*>(w[k].kind() == 2 ? a.c.v : a.c.k) + at + (int64_t)(h0 + w[k].h()) * PAGE * dim;
-        if (w[k].kind() == 0) store_turn(v[k], dst, w[k].u(), r, cs + w[k].t() * half);
-        else if (w[k].kind() == 1) store_plain(v[k], dst + other_channel(r, w[k].u(), kinds.width), kinds.width);
-        else store_plain(v[k], dst + 16 * w[k].u(), 16);
+        for (int k = 0; k < kUnits<In>; ++k)
+            if (threadIdx.x + k * kThreads < total) store(v[k], w[k]);
+    } else {
+        // Bounds out of order: each sequence whose own bounds are in order gets its rows, and
+        // a row may belong to several of them.
+        for (int b = 0; b < a.c.batch; ++b) {
+            if (max(cu[b], t0) >= min(cu[b + 1], t0 + nt)) continue;
+            __syncthreads();  // the sequence before has been written
+            if (threadIdx.x < nt) locate(b);
+            __syncthreads();
+            turns();
+            __syncthreads();
+#pragma unroll 1
+            for (int i = threadIdx.x; i < total; i += kThreads) {
+                const Where at = where(i, nt, nh, per_token, kinds);
+                Unit<In> x;
+                load(x, at);
+                store(x, at);
+            }
+        }
     }
     if (a.start && blockIdx.x == 0 && blockIdx.y == 0) count_tokens(a, cu, threadIdx.x, kThreads);
 }
@@ -403,7 +439,7 @@ void tile_rows(int64_t tokens, int heads, int units, int half, int most, int& tt
     const int parts = (heads * units + per - 1) / per;  // of a token's heads
     ht = std::min((heads + parts - 1) / parts, per / units);
     tt = ht < heads ? 1 : per / (units * heads);
-    tt = (int)std::min<int64_t>(std::min(tt, 64), tokens);
+    tt = (int)std::min<int64_t>(std::min(tt, kMaxTokens), tokens);
     if (half > 0) tt = std::min(tt, 4096 / half);  // 32 KB of (cos, sin)
 }
 

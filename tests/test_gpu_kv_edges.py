@@ -51,3 +51,39 @@ def test_windows_that_hide_nothing(csa, dtype, cache, window, new, H, hk):
     assert torch.equal(out, want) and torch.equal(lse, wlse)
     r = sum(new[:3])
     assert (out[r:r + new[3]] == 0).all() and torch.isneginf(lse[r:r + new[3]]).all()
+
+
+@pytest.mark.parametrize("how", ["start", "held", "alias"])
+@pytest.mark.parametrize("by", [1, 50])
+@pytest.mark.parametrize("cu,total,max_new", [
+    ([0, 10, 5, 20, 30], 30, 15),       # the second sequence's bounds decrease; rows 5 to 9 are the first's and the third's
+    ([0, 12, 4, 9, 9, 14], 14, 12),
+    ([0, 100, 5, 12], 12, 12),          # a bound beyond the rows
+    ([-3, 4, 2, 12, 11, 1, 6], 12, 10),
+    ([0, 3, 9, 9, 12], 12, 6),          # in order
+    ([20, 1, 20, 1, 20], 20, 20),
+])
+def test_append_takes_each_sequence_by_its_own_bounds(csa, how, by, cu, total, max_new):
+    """A sequence whose bounds are in order gets its rows, whatever the bounds of the others are."""
+    cu, total, max_new, B = [x * by for x in cu], total * by, max_new * by, len(cu) - 1
+    c = make(csa, [3 + 40 * b for b in range(B)], [max_new] * B, 2, 2, 64, BF, BF, seed=22)
+    start = c.n_tokens.clone()
+    c.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(total, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    wk, wv, wn = c.k_pages.clone(), c.v_pages.clone(), start.tolist()
+    offends = False
+    for b in range(B):
+        lo, hi = cu[b], cu[b + 1]
+        if not 0 <= lo <= hi <= total or hi - lo > max_new:
+            offends = True
+            continue
+        at = torch.arange(wn[b], wn[b] + hi - lo, device="cuda")
+        for pool, x in ((wk, k), (wv, v)):
+            pool.permute(0, 2, 1, 3)[c.table[b, at // 64].long(), at % 64] = x[lo:hi]
+        wn[b] += hi - lo
+    csa.kv_append(c.desc, k, v, c.cu, max_new, start={"start": start, "held": None, "alias": c.n_tokens}[how])
+    torch.cuda.synchronize()
+    assert c.status[0].item() == (csa.DEVERR_COUNT if offends else 0)
+    assert c.n_tokens.tolist() == wn
+    assert torch.equal(bits(c.k_pages), bits(wk)) and torch.equal(bits(c.v_pages), bits(wv))
