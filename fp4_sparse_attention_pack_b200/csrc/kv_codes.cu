@@ -337,7 +337,9 @@ __device__ void role_q(Smem<kDim, R>& sm, const KvAttn& a, int g, Cursor<R> cur)
             if constexpr (kBf) big = __uint_as_float(top << 16);
             else big = __half2float(__ushort_as_half((unsigned short)top));
             const int e = big == 0.0f ? 0 : 7 - ((int)max(__float_as_uint(big) >> 23, 1u) - 127);
-            const float f1 = pow2i(e / 2), f2 = pow2i(e - e / 2);
+            // E4M3 has no infinity: a row that holds one becomes NaN, as its softmax is (its
+            // scores are infinities, or NaN)
+            const float f1 = big < INFINITY ? pow2i(e / 2) : NAN, f2 = pow2i(e - e / 2);
 #pragma unroll
             for (int k = 0; k < kCh; ++k) {
                 const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};

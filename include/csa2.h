@@ -617,7 +617,9 @@ size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new
  * window > 0 only those with j > p - window:
  *   s_j = scale * q[t][h] . k[j][h / (H / kv_heads)],
  *   out[t][h] = sum_j softmax_j(s) v[j],   lse[t][h] = log(sum_j e^s_j).
- * A token that sees no key (p < 0) gives zeros and lse = -infinity.
+ * A token that sees no key (p < 0) gives zeros and lse = -infinity.  So does one
+ * whose scores are all -infinity, but a query with an infinite channel over E4M3
+ * pages gives NaN where max_new * H / kv_heads is at most 32.
  *   q, out  [total][H][head_dim], dtype CSA2_DTYPE_BF16 or _F16 (a cache of 16
  *           bits has the same type); out must not overlap q;
  *   lse     fp32 [total][H], or NULL.

@@ -87,3 +87,27 @@ def test_append_takes_each_sequence_by_its_own_bounds(csa, how, by, cu, total, m
     assert c.status[0].item() == (csa.DEVERR_COUNT if offends else 0)
     assert c.n_tokens.tolist() == wn
     assert torch.equal(bits(c.k_pages), bits(wk)) and torch.equal(bits(c.v_pages), bits(wv))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[1, 1], [4, 2], [8, 3], [30, 5], [200, 140]])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_infinite_queries(csa, dtype, cache, dim, new, value):
+    """A channel of a query is infinite: its scores are infinities of both signs, so the row is NaN, and only the row."""
+    c = make(csa, [150, 90], new, 8, 2, dim, dtype, cache, seed=23)
+    c.hold_all()
+    good, glse = c.attend(0.1)
+    c.q[0, 3, 5] = value
+    c.q[new[0], 6] = value
+    out, lse = c.attend(0.1)
+    torch.cuda.synchronize()
+    keep = torch.ones(c.total, 8, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 3), (new[0], 6)):
+        assert out[t, h].isnan().all() and lse[t, h].isnan()
+        keep[t, h] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
+    c.n_tokens[0] = new[0] - 1  # the first token sees no key
+    out, lse = c.attend(0.1)
+    torch.cuda.synchronize()
+    assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
