@@ -560,9 +560,10 @@ __device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& 
             }
             if (m == kNone) m = -INFINITY;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (f.first ? 1 : 0);
-            const float inv = !whole ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
+            const bool none = whole && s == 0.0f;  // no key was seen: zeros, whatever the sums hold
+            const float inv = whole ? 1.0f / s : 1.0f;
             if (thr < f.rows) {
-                sm.join[thr] = make_float2(w0 * inv, w1 * inv);
+                sm.join[thr] = none ? make_float2(-1.0f, 0.0f) : make_float2(w0 * inv, w1 * inv);
                 if (!whole) {
                     parts.ml[slot * R + thr] = make_float2(m, s);
                 } else if (a.lse) {
@@ -583,6 +584,7 @@ __device__ void role_softmax(Smem<kDim, R>& sm, const KvAttn& a, const KvParts& 
                     const float2 w = sm.join[r];
                     float v = nb > 0 ? o0[r] * w.x : 0.0f;
                     if (both) v = fmaf(o1[r], w.y, v);
+                    if (w.x < 0.0f) v = 0.0f;
                     if (!whole) po[r * kDim] = v;
                     else out[tok * a.out.ts + hd * a.out.hs] = (uint16_t)(pack16(v, 0.0f, kBf) & 0xFFFF);
                     if (++hd == g) hd = 0, ++tok;

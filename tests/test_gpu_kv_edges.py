@@ -111,3 +111,19 @@ def test_infinite_queries(csa, dtype, cache, dim, new, value):
     out, lse = c.attend(0.1)
     torch.cuda.synchronize()
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,H,hk", [([6, 3], 8, 8), ([6, 3], 8, 2), ([40, 8], 8, 2), ([300, 4], 4, 2)])
+def test_rows_that_see_no_key_are_zero(csa, dtype, cache, dim, new, H, hk):
+    """More tokens than are held, and a value that is NaN where only later tokens see it."""
+    c = make(csa, [0, 0], new, H, hk, dim, dtype, cache, seed=24)
+    held = [2, 3]
+    c.n_tokens.copy_(torch.tensor(held, dtype=torch.int32))
+    c.v_pages[c.table[0, 0].long(), :, 1, 7] = torch.full((), math.nan, device="cuda").to(cache)
+    out, lse = c.attend(0.2)
+    torch.cuda.synchronize()
+    for lo, m, n in ((0, new[0], held[0]), (new[0], new[1], held[1])):
+        assert (out[lo:lo + m - n] == 0).all() and torch.isneginf(lse[lo:lo + m - n]).all()
+        assert lse[lo + m - n:lo + m].isfinite().all()
