@@ -68,6 +68,131 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, int e) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Values that are not finite.  A key that some rows of an item see and others do not has
+// probability 0 for the others, but 0 x NaN and 0 x infinity are NaN.  So such elements
+// are taken out of V before the product (drop_unfinite), and when the CTA's results are
+// written the rows that see the key take them back (give_back).  Keys that all rows see
+// need none of it.  (Taking them back at each item's end cost the E4M3 chunk kernel 5 to
+// 14% in registers.)
+template <int kMode>
+__device__ __forceinline__ bool drop_unfinite(uint4& v) {
+    constexpr uint32_t kTop = is_e4m3(kMode) ? 0x7F7F7F7Fu : kMode == kBf16 ? 0x7F807F80u : 0x7C007C00u;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hit = is_e4m3(kMode) ? __vcmpeq4(w[i] & kTop, kTop) : __vcmpeq2(w[i] & kTop, kTop);
+        w[i] &= ~hit;
+        any |= hit;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+    return any != 0;
+}
+// Element c of a row of V where it is not finite, else 0.
+template <int kMode>
+__device__ __forceinline__ float unfinite_at(const uint8_t* row, int c) {
+    if constexpr (is_e4m3(kMode)) return (row[c] & 0x7F) == 0x7F ? NAN : 0.0f;
+    constexpr uint32_t kTop = kMode == kBf16 ? 0x7F80u : 0x7C00u;
+    const uint32_t h = reinterpret_cast<const uint16_t*>(row)[c];
+    if ((h & kTop) != kTop) return 0.0f;
+    return kMode == kBf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+}
+// An output element plus such a value.
+template <bool kBf>
+__device__ __forceinline__ void add16(uint16_t* at, float x) {
+    const float y = kBf ? __uint_as_float((uint32_t)*at << 16) : __half2float(__ushort_as_half(*at));
+    *at = (uint16_t)(pack16(y + x, 0.0f, kBf) & 0xFFFF);
+}
+
+// The keys that every row of an item sees; others are seen by some rows or by none.
+struct KvCommon {
+    int lo, hi;
+    __device__ __forceinline__ KvCommon(const KvFrag& f, int window) : lo(first_key(f.v.hi, window)), hi(f.s.n - f.s.m + f.v.t0) {}
+    __device__ __forceinline__ bool has(int key) const { return key >= lo && key <= hi; }
+    // a block with keys that it does not hold
+    __device__ __forceinline__ bool leaves(int key0, int keys) const { return key0 < lo || key0 + keys - 1 > hi; }
+};
+
+// Whether any of the chunks that it has seen holds such an element.
+template <int kMode>
+struct Unfinite {
+    uint32_t bits[4] = {0, 0, 0, 0};  // sums of 0 x the elements, or bit 7 of each code that is NaN
+    __device__ __forceinline__ void see(const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (is_e4m3(kMode)) bits[i] |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
+            else if constexpr (kMode == kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(bits[i]) : "r"(w[i]), "r"(0u));
+            else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(bits[i]) : "r"(w[i]), "r"(0u));
+        }
+    }
+    __device__ __forceinline__ bool any() const {
+        return ((bits[0] | bits[1] | bits[2] | bits[3]) & (is_e4m3(kMode) ? 0x80808080u : 0x7FFF7FFFu)) != 0;
+    }
+};
+
+// A warp's pass over a block of V in shared memory (kSlabs slabs of kBlk rows of kRowBytes)
+// that not all rows of the item see: rows that none sees become 0, and the others lose what
+// is not finite.  True if a value was taken out.
+template <int kMode, int kBlk, int kRowBytes, int kSlabs, class Unseen>
+__device__ __forceinline__ bool clear_rows(uint8_t* block, const KvCommon& common, int key0, const Unseen& unseen) {
+    constexpr int kSteps = kSlabs * kBlk * kRowBytes / 512;  // of 512 bytes
+    const int lane = threadIdx.x & 31;
+    uint4* const at = reinterpret_cast<uint4*>(block) + lane;
+    const auto row = [&](int k) { return (k * 512 + lane * 16) / kRowBytes % kBlk; };
+#pragma unroll 4
+    for (int k = 0; k < kSteps; ++k)
+        if (unseen(row(k))) at[32 * k] = make_uint4(0, 0, 0, 0);
+    Unfinite<kMode> found;  // (a lane reads what it has written)
+#pragma unroll 4
+    for (int k = 0; k < kSteps; ++k)
+        if (!common.has(key0 + row(k))) found.see(at[32 * k]);
+    if (!__any_sync(0xffffffffu, found.any())) return false;
+#pragma unroll 1
+    for (int k = 0; k < kSteps; ++k) {
+        if (common.has(key0 + row(k))) continue;
+        uint4 v = at[32 * k];
+        if (drop_unfinite<kMode>(v)) at[32 * k] = v;
+    }
+    return true;
+}
+
+// The CTA's results are written; `threads` of its threads add what was taken out to the
+// rows that see it.  Thread = channel of every few rows.
+template <int kMode, int kDim, int kRows, int kBlk, bool kRowsFast, class Cursor>
+__device__ __forceinline__ void give_back(const KvAttn& a, const KvParts& parts, int g, Cursor cur, int threads) {
+    const int c = threadIdx.x % kDim;
+    KvFrag f;
+    while (cur.next(a, g, f)) {
+        const KvCommon common(f, a.window);
+        const int end = min(f.f1 * kBlk - 1, f.v.hi);
+#pragma unroll 1
+        for (int key = max(f.f0 * kBlk, f.v.lo); key <= end; ++key) {
+            if (common.has(key)) {
+                key = common.hi;
+                continue;
+            }
+            const int page = a.c.page_table[(int64_t)f.b * a.c.max_pages + key / PAGE];
+            if (page < 0 || page >= a.c.num_pages) continue;
+            const int64_t row = ((int64_t)page * a.c.kv_heads + f.h) * PAGE + key % PAGE;
+            const float x = unfinite_at<kMode>(a.c.v + row * kDim * (is_e4m3(kMode) ? 1 : 2), c);
+            if (x == 0.0f) continue;
+#pragma unroll 1
+            for (int r = threadIdx.x / kDim; r < f.rows; r += threads / kDim) {
+                const int q = f.tile * kRows + r, token = q / g, pos = f.s.n - f.s.m + token;
+                if (key > pos || key < first_key(pos, a.window)) continue;
+                if (f.first && f.last) {
+                    add16<kMode == kBf16 || kMode == kE4m3Bf16>(
+                        reinterpret_cast<uint16_t*>(a.out.p) + (int64_t)(f.s.row0 + token) * a.out.ts +
+                            (int64_t)(f.h * g + q - token * g) * a.out.hs + c, x);
+                } else {
+                    float* part = reinterpret_cast<float*>(parts.o) + (2 * (int64_t)blockIdx.x + (f.first ? 1 : 0)) * kRows * kDim;
+                    part[kRowsFast ? (c / 4 * kRows + r) * 4 + c % 4 : r * kDim + c] += x;
+                }
+            }
+        }
+    }
+}
+
 // The items that cuts divide.  A thread joins four channels of a row, four loads in
 // flight; when the items have many partial results each (few long sequences), 4 or
 // 16 threads take every 4th or 16th of them and meet in shared memory, in a fixed

@@ -77,6 +77,8 @@ struct Smem {
     float c[2][R];                                // softmax scale of each row (per item parity)
     int pos[2][R];                                // its last key
     uint8_t bad[kRing];                           // bit p: page p of the block is outside the pool
+    int unfinite;                                 // values were taken out
+    KvCursor<R, kBlk, kOver> cur;                 // the CTA's, for them
     uint64_t full[kPlaces], empty[kPlaces];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], tail, drained;
     uint64_t frag_full[2], frag_empty[2], pair_full, pair_empty;
@@ -227,6 +229,7 @@ __device__ void role_tma(Smem<kDim, R>& sm, const KvAttn& a, const KvMaps& maps,
     while (alive && cur.next(a, g, f)) {
         const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
         const int nb = f.f1 - f.f0, first = f.v.lo / PAGE, last = f.v.hi / PAGE;
+        const KvCommon common(f, a.window);
         int ids = -1, have = -1;  // 32 page ids at a time, one to a lane
         for (int x = 0; x < nb && alive; ++x) {
             const int j = f.f0 + x;
@@ -254,7 +257,7 @@ __device__ void role_tma(Smem<kDim, R>& sm, const KvAttn& a, const KvMaps& maps,
                 __syncwarp();
             }
             // rows of V that no query sees are zeroed when they are there, as 0 x NaN is not 0
-            const bool part = kV && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
+            const bool part = kV && (common.leaves(j * kBlk, kBlk) || bad);
             uint64_t* bar = part ? &sm.tail : &sm.full[place];
             const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * kPage;
             if (!part || bytes) {
@@ -278,11 +281,11 @@ __device__ void role_tma(Smem<kDim, R>& sm, const KvAttn& a, const KvMaps& maps,
                 }
                 ++tails;
             }
-            for (int i = lane; i < kBlk * kDim / 16; i += 32) {
-                const int r = i / (kDim / 16), key = j * kBlk + r;
-                if (key < f.v.lo || key > f.v.hi || (bad >> (r >> 6) & 1))
-                    *reinterpret_cast<uint4*>(&sm.kv[place][16 * i]) = make_uint4(0, 0, 0, 0);
-            }
+            const auto unseen = [&](int r) {
+                const int key = j * kBlk + r;
+                return key < f.v.lo || key > f.v.hi || (bad >> (r >> 6) & 1);
+            };
+            if (clear_rows<kE4m3Bf16, kBlk, kDim, 1>(sm.kv[place], common, j * kBlk, unseen)) sm.unfinite = 1;
             fence_proxy_async_smem();
             __syncwarp();
             mbar_arrive_w(&sm.full[place]);
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.tail, 1);
         mbar_init(&sm.drained, 1);
         sm.abort = 0;
+        sm.unfinite = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -642,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
     const Cursor<R> cur = kv_plan<R, kBlk, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    if (tid == 0) sm.cur = cur;
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     tc_fence_before();
     __syncthreads();
@@ -673,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tb, kTmemCols);
     }
+    if (sm.unfinite && warp < 8) give_back<kBf ? kE4m3Bf16 : kE4m3F16, kDim, R, kBlk, false>(a, parts, plan.g, sm.cur, 256);
 }
 
 template <int kDim, int R, bool kBf>

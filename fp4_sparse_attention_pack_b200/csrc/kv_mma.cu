@@ -28,7 +28,10 @@
 //                    undone in c.
 // Rows of V that no row of the item sees (behind the last key, before the
 // window, on a page that is not loaded) are zeroed in shared memory, because
-// 0 x NaN would reach the sums; their scores are masked.
+// 0 x NaN would reach the sums; their scores are masked.  Of rows that only some
+// rows see, what is not finite is taken out and given back at the end
+// (kv_attn.cuh); the pass that looks for it costs 12 prompts of up to 512 through a
+// window of 128 some 2 us of 31, other calls 1% or less.
 //
 // A chunk of 2,048 tokens over 16,384, 64 / 8 heads of 128, bf16: 1.05 ms (984
 // TFLOP/s, 58% of the burst rate, 69% of the sustained one).  A block takes 3,650
@@ -88,6 +91,8 @@ struct Smem {
     uint8_t raw[kRaw][is_e4m3(kMode) ? kBlk * kDim : 16];  // slabs of 64 channels [key][64]
     uint8_t qe[2][kMode == kE4m3Bf16 ? kTile : 8];  // power of two of each row, + kExp (per item parity)
     uint8_t bad[kRing];                         // bit p: page p of the block is outside the pool
+    int unfinite;                               // values were taken out
+    KvCursor<kTile, kBlk, kOver> cur;           // the CTA's, for them
     uint64_t full[kStages + 1], empty[kStages + 1];
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t q_full, q_empty;
@@ -300,7 +305,7 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
         }
     };
     // block j's K or V to the next place of the ring
-    auto put = [&](const PagePair& pp, int j, int place, bool is_v) {
+    auto put = [&](const PagePair& pp, int j, int place, bool is_v, const KvCommon& common) {
         if (used >= places && !wait_bar_warp(sm, &empties[ring.i], ring.phase ^ 1)) return false;
         ++used;
         uint64_t* full = &fulls[ring.i];
@@ -312,7 +317,7 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
             }
             __syncwarp();
         }
-        if (kRawCodes || !is_v || (j * kBlk >= f.v.lo && j * kBlk + kBlk - 1 <= f.v.hi && !pp.bad)) {
+        if (kRawCodes || !is_v || !(common.leaves(j * kBlk, kBlk) || pp.bad)) {
             mbar_expect_tx_w(full, bytes);
             load(pp, is_v, f.h, full);
         } else {
@@ -326,11 +331,8 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
                 }
                 ++tails;
             }
-            for (int i = lane; i < kBlk * S::kSlabs * 8; i += 32) {
-                const int r = (i >> 3) % kBlk;
-                if (v_row_unseen(f, pp.bad, j, r))
-                    *reinterpret_cast<uint4*>(&sm.kv[ring.i][i / (8 * kBlk)][r * 128 + (i & 7) * 16]) = make_uint4(0, 0, 0, 0);
-            }
+            if (clear_rows<kMode, kBlk, 128, S::kSlabs>(sm.kv[ring.i][0], common, j * kBlk, [&](int r) { return v_row_unseen(f, pp.bad, j, r); }))
+                sm.unfinite = 1;
             fence_proxy_async_smem();
             __syncwarp();
             mbar_arrive_w(full);
@@ -342,6 +344,7 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
     while (alive && cur.next(a, g, f)) {
         const int32_t* table = a.c.page_table + (int64_t)f.b * a.c.max_pages;
         const int nb = f.f1 - f.f0, ahead = one_tile(f) ? 1 : 0;
+        const KvCommon common(f, a.window);
         int ids = -1, have = -1;  // 32 page ids at a time, one to a lane
         PagePair pp = {{-1, -1}, 0};
         for (int x = -ahead; x < nb && alive; ++x) {  // K of block x + ahead, then V of block x
@@ -354,9 +357,9 @@ __device__ void role_tma(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& m
                     ids = pg >= f.v.lo / PAGE && pg <= f.v.hi / PAGE ? table[pg] : -1;
                 }
                 pp = pages_of(a, f, j, __shfl_sync(0xffffffffu, ids, 2 * j & 31), __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31));
-                alive = put(pp, j, blocks + x + ahead, false);
+                alive = put(pp, j, blocks + x + ahead, false, common);
             }
-            if (x >= 0 && alive) alive = put(ahead ? before : pp, f.f0 + x, 0, true);
+            if (x >= 0 && alive) alive = put(ahead ? before : pp, f.f0 + x, 0, true, common);
         }
         blocks += nb;
     }
@@ -380,8 +383,8 @@ __device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
 // A block of codes, slabs of 64 channels [key][64], to fp16 as the MMAs read it: a warp
 // takes 8 rows of a slab at a time, 512 bytes to 1,024, four lanes to a row (the two
 // rows of a quarter warp write all eight chunks of a line).
-template <int kDim, int kUnroll, class Seen>
-__device__ __forceinline__ void widen(const uint8_t* raw, uint8_t* kv, int thread, const Seen& seen) {
+template <int kDim, int kUnroll, class Clear>
+__device__ __forceinline__ void widen(const uint8_t* raw, uint8_t* kv, int thread, const Clear& clear) {
     constexpr int kAll = kBlk * kDim / 512;
     const int lane = thread & 31, r8 = lane >> 2;
     const uint8_t* src = raw + 16 * lane;
@@ -390,7 +393,7 @@ __device__ __forceinline__ void widen(const uint8_t* raw, uint8_t* kv, int threa
 #pragma unroll kUnroll
     for (int u = thread >> 5; u < kAll; u += kGroupWarps) {
         uint4 v = *reinterpret_cast<const uint4*>(src + 512 * u), lo, hi;
-        if (!seen((8 * u + r8) % kBlk)) v = make_uint4(0, 0, 0, 0);
+        clear((8 * u + r8) % kBlk, v);
         widen16(v, lo, hi);
         *reinterpret_cast<uint4*>(lo_at + 1024 * u) = lo;
         *reinterpret_cast<uint4*>(hi_at + 1024 * u) = hi;
@@ -461,6 +464,7 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
             const uint32_t stages = stages_of<S>(a, g);
             const int nb = f.f1 - f.f0, group = tid / (32 * kGroupWarps), gt = tid % (32 * kGroupWarps);
             const bool one = one_tile(f);
+            const KvCommon common(f, a.window);
             constexpr int kGroups = kLoaders / (32 * kGroupWarps);
             // a place's parity says which turn of the ring it is only within one turn
             static_assert(kGroups <= S::kStages && kGroups <= S::kRaw, "more groups than places");
@@ -472,12 +476,24 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
                 if (place >= stages && !wait_bar_warp(sm, &sm.empty[ri], (place / stages - 1) & 1)) return;
                 if (!wait_bar_warp(sm, &sm.raw_full[rw], (place / S::kRaw) & 1)) return;
                 const int bad = sm.bad[(blocks + part.j) % kRing];
-                const bool zero = part.is_v && (j * kBlk < f.v.lo || j * kBlk + kBlk - 1 > f.v.hi || bad);
-                const auto seen = [&](int r) { return !zero || !v_row_unseen(f, bad, j, r); };
                 // Two tiles' softmax warps need the issue slots, so few loads are in flight
                 // then; for one tile widening is what bounds the kernel.
-                if (one) widen<kDim, 4>(sm.raw[rw], sm.kv[ri][0], gt, seen);
-                else widen<kDim, 2>(sm.raw[rw], sm.kv[ri][0], gt, seen);
+                const auto nothing = [](int, uint4&) {};
+                if (part.is_v && (common.leaves(j * kBlk, kBlk) || bad)) {
+                    Unfinite<kMode> found;
+                    widen<kDim, 2>(sm.raw[rw], sm.kv[ri][0], gt, [&](int r, uint4& v) {
+                        if (v_row_unseen(f, bad, j, r)) v = make_uint4(0, 0, 0, 0);
+                        if (!common.has(j * kBlk + r)) found.see(v);
+                    });
+                    if (__any_sync(0xffffffffu, found.any())) {  // once more, without them
+                        widen<kDim, 1>(sm.raw[rw], sm.kv[ri][0], gt, [&](int r, uint4& v) {
+                            if (v_row_unseen(f, bad, j, r)) v = make_uint4(0, 0, 0, 0);
+                            if (!common.has(j * kBlk + r)) drop_unfinite<kMode>(v);
+                        });
+                        sm.unfinite = 1;
+                    }
+                } else if (one) widen<kDim, 4>(sm.raw[rw], sm.kv[ri][0], gt, nothing);
+                else widen<kDim, 2>(sm.raw[rw], sm.kv[ri][0], gt, nothing);
                 fence_proxy_async_smem();
                 __syncwarp();
                 mbar_arrive_w(&sm.full[ri]);
@@ -779,6 +795,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         mbar_init(&sm.tail, 1);
         mbar_init(&sm.drained, 1);
         sm.abort = 0;
+        sm.unfinite = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -787,6 +804,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
     if (tid == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
     Cursor cur = kv_plan<kTile, kBlk, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    if (tid == 0) sm.cur = cur;
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     tc_fence_before();
     __syncthreads();
@@ -819,6 +837,7 @@ __global__ void __launch_bounds__(threads_of(kMode), 1)
         tc_fence_after();
         tmem_dealloc(tb, kTmemCols);
     }
+    if (sm.unfinite && warp < 8) give_back<kMode, kDim, kTile, kBlk, true>(a, parts, plan.g, sm.cur, 256);
 }
 
 template <int kDim, int kMode>

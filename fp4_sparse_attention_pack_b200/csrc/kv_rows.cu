@@ -57,6 +57,8 @@ struct __align__(1024) Smem {
     float red[2][kRows][kDim];
     float ml[kWarps][kRows][2];
     uint8_t bad[kStages];
+    int unfinite;  // values were taken out
+    KvCursor<kRows, PAGE, kOver> cur;  // the CTA's, for them
     uint64_t full[kStages], empty[kStages];
     int abort;
 };
@@ -160,6 +162,27 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, const KvMaps& 
 
 // ---------------------------------------------------------------- rows
 
+// A warp takes what is not finite out of its 16 rows of V that some rows of the item see
+// and others do not; true for a lane that found such a value.
+template <int kDim, int kMode>
+__device__ __forceinline__ bool drop_rows(uint8_t* page, int row0, int page_key, KvCommon common) {
+    const int lane = threadIdx.x & 31;
+    bool any = false;
+    for (int i = lane; i < 16 * (kDim / 8); i += 32) {
+        const int r = row0 + (i & 15);
+        if (common.has(page_key + r)) continue;
+        uint4* at = reinterpret_cast<uint4*>(page + at16(r, i >> 4));
+        uint4 v = *at;
+        if (drop_unfinite<kMode>(v)) {
+            *at = v;
+            any = true;
+        }
+    }
+    fence_proxy_async_smem();  // the stage is next written by a TMA
+    __syncwarp();
+    return any;
+}
+
 template <int kDim, int kMode>
 __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts& parts, int64_t per, int g,
                           Cursor cur) {
@@ -241,6 +264,8 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                 }
                 // ---- softmax: elements 0, 1 of row quad, 2, 3 of row quad + 8
                 if (kb + 15 > pos_min || kb < lo_max) {
+                    if (f.s.m > 1 && drop_rows<kDim, kMode>(sm.kv[st][1], 16 * warp, kb - 16 * warp, KvCommon(f, a.window)))
+                        sm.unfinite = 1;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -386,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mbar_init(&sm.empty[i], kWarps);
         }
         sm.abort = 0;
+        sm.unfinite = 0;
         fence_mbar_init();
     }
     cudaTriggerProgrammaticLaunchCompletion();
@@ -393,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (threadIdx.x == 0) parts.cut[blockIdx.x].last = -1;
     int64_t per;
     const Cursor cur = kv_plan<kRows, PAGE, kOver, kSnap>(a, plan, *reinterpret_cast<KvPlanSmem*>(sm.kv), &per);
+    if (threadIdx.x == 0) sm.cur = cur;
     fence_proxy_async_smem();  // the plan's arrays were written by ordinary stores
     __syncthreads();
     if (threadIdx.x < 32 * kWarps) role_rows<kDim, kMode>(sm, a, parts, per, plan.g, cur);
@@ -400,6 +427,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncwarp();
     __syncthreads();
     if (sm.abort && threadIdx.x == 0) atomicOr(a.c.status, CSA2_DEVERR_TIMEOUT);
+    if (sm.unfinite && threadIdx.x < 32 * kWarps)
+        give_back<kMode, kDim, kRows, PAGE, false>(a, parts, plan.g, sm.cur, 32 * kWarps);
 }
 
 template <int kDim, int kMode>

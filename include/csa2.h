@@ -557,7 +557,8 @@ int csa2_rotate(const csa2_rotary* rot, const csa2_heads* x, const csa2_heads* y
  * (CSA2_ERR_UNSUPPORTED beyond).  A CSA2_KV_E4M3 cache holds the nearest E4M3
  * value (ties to even, saturating at +-448), without a scale, like the FP8
  * window.  `status` collects CSA2_DEVERR_* bits.  Rows of a page behind
- * n_tokens may hold anything, NaN included: they never reach a result.
+ * n_tokens may hold anything, NaN included: they never reach a result.  A key and
+ * its value reach only the tokens that see the key, NaN and infinities too.
  */
 #define CSA2_KV_BF16 0
 #define CSA2_KV_F16 1

@@ -127,3 +127,44 @@ def test_rows_that_see_no_key_are_zero(csa, dtype, cache, dim, new, H, hk):
     for lo, m, n in ((0, new[0], held[0]), (new[0], new[1], held[1])):
         assert (out[lo:lo + m - n] == 0).all() and torch.isneginf(lse[lo:lo + m - n]).all()
         assert lse[lo + m - n:lo + m].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("old,new,H,hk,window", [
+    ([70, 200], [4, 3], 8, 4, 0),        # at most 16 rows to a kv head
+    ([126, 9000, 60], [4, 4, 3], 8, 2, 0),
+    ([5000, 64], [8, 5], 8, 2, 0),       # 32; a long sequence over many CTAs
+    ([3000, 90], [5, 4], 6, 2, 100),
+    ([900, 120], [16, 9], 8, 2, 0),      # one tile of the chunk kernel
+    ([300, 40], [150, 70], 8, 4, 0),     # two
+    ([300, 40], [150, 70], 6, 2, 50),
+    ([900], [300], 2, 2, 0),
+    ([20000], [70], 16, 2, 10000),
+])
+def test_values_that_are_not_finite_reach_the_tokens_that_see_them(csa, dtype, cache, dim, old, new, H, hk, window):
+    """A key that only later tokens see, or only earlier ones through a window, in the same call: its NaN or infinity is
+    no part of the others' sums."""
+    c = make(csa, old, new, H, hk, dim, dtype, cache, seed=25)
+    c.hold_all()
+    scale = dim ** -0.5
+    good, glse = c.attend(scale, window)
+    want = good.clone()
+    g, row = H // hk, 0
+    for b, (o, m) in enumerate(zip(old, new)):
+        at = torch.arange(o, o + m, device="cuda")
+        places = [(o + m - 1, 3, math.inf), (o + m // 2, 4, math.nan), (o + 1, 5, -math.inf), (o + m - 1, 6, math.nan)]
+        if window:
+            places += [(max(0, o - window + 2), 7, math.inf), (max(0, o + m // 2 - window + 1), 8, math.nan)]
+        for j, ch, x in places:
+            if cache == E4:
+                x = math.nan
+            c.v_pages[c.table[b, j // 64].long(), hk - 1, j % 64, ch] = torch.full((), x, device="cuda").to(cache)
+            see = (at >= j) & ((at < j + window) if window else at >= 0)
+            want[row:row + m, H - g:, ch] = torch.where(see[:, None], x, want[row:row + m, H - g:, ch])
+        row += m
+    out, lse = c.attend(scale, window)
+    torch.cuda.synchronize()
+    assert torch.equal(lse, glse)
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
