@@ -21,6 +21,13 @@ constexpr float kGap = 8.0f;  // log2 units by which a block may exceed the maxi
 enum Mode { kBf16, kF16, kE4m3Bf16, kE4m3F16 };
 constexpr bool is_e4m3(int mode) { return mode >= kE4m3Bf16; }
 
+// By how much (log2 units) the reference of a row's exponentials is below the maximum when
+// it is taken, where probabilities are rounded to fp16 (kv_mma.cu, kv_rows.cu).  The
+// largest then lies in [2^7, 2^15], so half a step of fp16's subnormals, which smaller
+// ones fall into, is 2^-32 of it: an attention sink may hide the keys behind it only by
+// that much.  bf16 has fp32's range.
+constexpr float below(int mode) { return mode == kBf16 ? 0.0f : 7.0f; }
+
 struct KvMaps {
     CUtensorMap k, v;
 };

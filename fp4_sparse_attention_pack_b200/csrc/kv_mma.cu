@@ -614,7 +614,7 @@ __device__ void role_softmax(Smem<kDim, kMode>& sm, const KvAttn& a, const KvPar
                     for (int k = 0; k < 4; ++k) masked(k, r[k]);
                     tmem_wait_st();
                 }
-                const float bm = fmaxf(fmaxf(max32(r[0]), max32(r[1])), fmaxf(max32(r[2]), max32(r[3]))) * c;
+                const float bm = fmaxf(fmaxf(max32(r[0]), max32(r[1])), fmaxf(max32(r[2]), max32(r[3]))) * c - below(kMode);
                 const bool move = bm > mref + kGap || (mref == -INFINITY && bm > -INFINITY);
                 if (__any_sync(0xffffffffu, move)) {
                     const float f1 = move ? ex2(mref - bm) : 1.0f;  // mref = -inf: 0

@@ -282,6 +282,7 @@ __device__ void role_rows(Smem<kDim, kMode>& sm, const KvAttn& a, const KvParts&
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     bm[e] = x * c0;
+                    bm[e] -= below(kMode);
                     move = move || bm[e] > mref[e] + kGap || (mref[e] == -INFINITY && bm[e] > -INFINITY);
                 }
                 if (__any_sync(0xffffffffu, move)) {

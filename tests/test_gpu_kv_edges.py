@@ -168,3 +168,48 @@ def test_values_that_are_not_finite_reach_the_tokens_that_see_them(csa, dtype, c
     assert torch.equal(lse, glse)
     assert torch.equal(out.isnan(), want.isnan())
     assert torch.equal(out.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+
+
+def far_keys(csa, old, new, H, hk, dim, dtype, cache, nats, step):
+    """One key of 16 has a score above all others by `nats`, and a value of 0: the others make the whole result.
+    Each of their probabilities is rounded once, and off by at most `step` times the largest one besides."""
+    c = make(csa, old, new, H, hk, dim, dtype, cache, seed=26)
+    c.hold_all()
+    c.q.fill_(1.0)
+    n = old[0] + new[0]
+    at = torch.arange(n, device="cuda")
+    sink = at % 16 == 5
+    k = torch.where(sink, 1.0, 0.0)[:, None, None].expand(n, hk, dim)
+    v = torch.rand(n, hk, dim, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") * 192 + 256
+    v = torch.where(sink[:, None, None], 0.0, v)
+    for pool, x in ((c.k_pages, k), (c.v_pages, v)):
+        pool.permute(0, 2, 1, 3)[c.table[0, at // 64].long(), at % 64] = x.to(cache)
+    v = v.to(cache).double()
+    out, lse = c.attend(nats / dim)
+    torch.cuda.synchronize()
+    pos = torch.arange(old[0], n, device="cuda")[:, None]
+    s = torch.where(at <= pos, torch.where(sink, float(np.float32(nats / dim)) * dim, 0.0).double(), -math.inf)
+    p = torch.softmax(s, -1)                                            # [tokens][keys]
+    want = torch.einsum("tj,jhd->thd", p, v).repeat_interleave(H // hk, 1)
+    sums = torch.einsum("tj,jhd->thd", (at <= pos).double(), v).repeat_interleave(H // hk, 1)
+    # scores are exact in fp32 but for scale log2 e and its product (2^-22 of nats each), exp2 and the polynomial 2^-18
+    eps = 2 * nats * 2.0 ** -21 + 2.0 ** -18 + (n / 8 + 64) * 2.0 ** -24
+    u_p, u_o = 2.0 ** -8 if cache == BF else 2.0 ** -11, 2.0 ** -8 if dtype == BF else 2.0 ** -11
+    err = (u_p + eps) * want + step * p.amax(-1)[:, None, None] * sums
+    bound = err + u_o * (want + err) + 2.0 ** -25
+    d = (out.double() - want).abs()
+    assert (d <= bound).all(), (d / bound).max()
+    l = torch.logsumexp(s, -1)[:, None]
+    assert ((lse.double() - l).abs() <= eps + 2.0 ** -23 * l.abs()).all()
+
+
+# (over E4M3 pages, calls of at most 32 rows to a kv head split their probabilities otherwise)
+@pytest.mark.parametrize("dtype,cache,old,new,H,hk", [
+    (dtype, cache, *size) for dtype, cache in TYPES
+    for size in (([3990], [1], 8, 2), ([3990], [4], 8, 4), ([2000], [20], 8, 2), ([1500], [300], 2, 2))
+    if cache != E4 or size[1][0] * size[2] // size[3] > 32])
+@pytest.mark.parametrize("nats", [12.0, 17.5, 18.4])
+def test_keys_far_below_the_largest_score(csa, dtype, cache, nats, old, new, H, hk):
+    """Probabilities of 2^-17 to 2^-26.5 of a row's largest one.  In fp16 the largest lies at 2^7 or above, so half a
+    step of its subnormals is 2^-32 of it (bf16 has none here)."""
+    far_keys(csa, old, new, H, hk, 128, dtype, cache, nats, 2.0 ** -32)
