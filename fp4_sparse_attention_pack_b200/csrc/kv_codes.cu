@@ -6,16 +6,18 @@
 // with N columns, each split into three E4M3 terms of four bits (12 bits together,
 // one more than fp16):
 //
-//   S^T [128 keys][3 R]     = K [128][128] . (q1 q2 q3)^T     s = S1 + S2 2^-4 + S3 2^-8
-//   O^T [128 channels][3 R] += V^T [128][128] . (p1 p2 p3)    o = O1 + O2 2^-4 + O3 2^-8
+//   S^T [128 keys][3 R]     = K [128][128] . (q1 q2 q3)^T     s = S1 + S2 2^-5 + S3 2^-10
+//   O^T [128 channels][3 R] += V^T [128][128] . (p1 p2 p3)    o = O1 + O2 2^-5 + O3 2^-10
 //
-// where x1 = rn(x), x2 = rn(2^4 (x - x1)), x3 = rn(2^4 (2^4 (x - x1) - x2)); R is 16 or
-// 32.  A row's queries are scaled by a power of two that takes the largest into
-// [2^7, 2^8), undone in the softmax scale; terms are exact to 2^-27 of it.
+// where x1 = rn(x), x2 = rn(2^5 (x - x1)), x3 = rn(2^5 (2^5 (x - x1) - x2)); R is 16 or
+// 32.  Of |x| <= 2^8 a rounding leaves at most 2^3, so 2^5 times it is in range again.
+// A row's queries are scaled by a power of two that takes the largest into [2^7, 2^8),
+// undone in the softmax scale; the third term is a multiple of 2^-19, so a query is
+// exact to 2^-20, 2^-27 of the largest.
 // Probabilities are rounded to fp16 first and then split.  The reference of a row's
 // exponentials is its maximum less 4 (log2) when it is taken, and moves when a score
 // exceeds it by more than 8: the largest probability lies in [2^4, 2^8], E4M3's range,
-// and the third term's rounding, 2^-18, is at most 2^-22 of it.  (Less 5 or 6 would
+// and the third term's rounding, 2^-20, is at most 2^-24 of it.  (Less 5 or 6 would
 // move it more often: 4 and 20% longer with 32 rows.)
 //
 // One CTA an SM, 384 threads, blocks of 128 keys:
@@ -132,11 +134,11 @@ __device__ __forceinline__ uint32_t h2_to_codes(uint32_t h) {  // two fp16 to tw
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
 }
-// The next term's value: 2^4 (h - its code).
+// The next term's value: 2^5 (h - its code).
 __device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t code) {
     uint32_t b = e4m3x2_to_h2(code), r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(b));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4C004C00u));  // 16
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x50005000u));  // 32
     return r;
 }
 // Two values of fp16 into three terms of two codes.
@@ -414,10 +416,10 @@ __device__ __forceinline__ void load_terms(uint32_t taddr, float (&v)[R]) {
     load_cols<R>(taddr, v);
     load_cols<R>(taddr + R, b);
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = fmaf(b[r], 0x1p-4f, v[r]);
+    for (int r = 0; r < R; ++r) v[r] = fmaf(b[r], 0x1p-5f, v[r]);
     load_cols<R>(taddr + 2 * R, b);
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = fmaf(b[r], 0x1p-8f, v[r]);
+    for (int r = 0; r < R; ++r) v[r] = fmaf(b[r], 0x1p-10f, v[r]);
 }
 
 // Waits that give up do not end the loops, so that a group's warps meet at the same

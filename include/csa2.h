@@ -628,7 +628,7 @@ size_t csa2_kv_attn_workspace(const csa2_kv_cache* cache, int total, int max_new
  * scale is positive.  Sums and softmax statistics
  * are fp32; the probabilities are rounded to the type of the cache's values
  * (fp16 for E4M3, whose values, and queries scaled by a power of two per row,
- * are exact within 2^27 of the row's largest magnitude) for the product
+ * are exact to 2^-27 of the row's largest magnitude) for the product
  * with them.  Keys on a page outside the pool are left out with
  * CSA2_DEVERR_PAGE; n_tokens outside [0, max_pages * 64] is clamped with
  * CSA2_DEVERR_COUNT.

@@ -213,3 +213,44 @@ def test_keys_far_below_the_largest_score(csa, dtype, cache, nats, old, new, H, 
     """Probabilities of 2^-17 to 2^-26.5 of a row's largest one.  In fp16 the largest lies at 2^7 or above, so half a
     step of its subnormals is 2^-32 of it (bf16 has none here)."""
     far_keys(csa, old, new, H, hk, 128, dtype, cache, nats, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nats", [10.0, 14.5, 15.7, 16.3])
+@pytest.mark.parametrize("old,new,H,hk", [([3990], [1], 8, 2), ([3990], [4], 8, 2), ([2000], [8], 8, 2)])
+def test_keys_far_below_the_largest_score_over_codes(csa, dtype, dim, nats, old, new, H, hk):
+    """The last of three E4M3 terms is a multiple of 2^-19 and the largest probability 2^4 or more: half a step is 2^-24
+    of it."""
+    far_keys(csa, old, new, H, hk, dim, dtype, E4, nats, 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("H", [16, 32])
+def test_small_channels_of_a_query_over_codes(csa, dtype, dim, H):
+    """A channel is kept to 2^-27 of the row's largest one: rows whose channels are all one small value, so that what its
+    terms lose adds up."""
+    rows = 10 * 128  # 2^-14 .. 2^-23 times 1 + i / 128
+    B = rows // H
+    c = make(csa, [3] * B, [1] * B, H, 1, dim, dtype, E4, seed=27)
+    c.hold_all()
+    i = torch.arange(rows, device="cuda")
+    small = (1 + (i % 128).double() / 128) * 2.0 ** (-14 - (i // 128)).double()
+    q = small[:, None].repeat(1, dim)
+    q[:, 0] = 1.0
+    c.q.copy_(q.view(B, H, dim).to(dtype))
+    q = c.q.double()
+    keys = torch.tensor([1.0, 0.5, -1.0, 0.75], device="cuda")[:, None].repeat(1, dim)
+    keys[:, 0] = 0.0
+    for j in range(4):
+        c.k_pages[c.table[:, 0].long(), 0, j] = keys[j].to(E4)
+    scale = 2.0 ** 11
+    out, lse = c.attend(scale)
+    torch.cuda.synchronize()
+    s = scale * torch.einsum("thc,jc->thj", q, keys.double())
+    want = torch.logsumexp(s, -1)
+    # each score is off by 2^-27 a channel; products and sums are exact in fp32 but for 2^-24 of their size, as is exp2
+    bound = scale * dim * 2.0 ** -27 + 2.0 ** -21 * (1 + s.abs().amax(-1))
+    d = (lse.double() - want).abs()
+    assert (d <= bound).all(), (d / bound).max()
