@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from ._build import BIND, LIB
+from ._build import LIB, bind_path
 
 __all__ = ["Csa2Error", "lib", "csa2_cache", "csa2_window", "csa2_model", "csa2_step_in",
            "csa2_step_out", "pack_cache", "index_topk", "index_topk_workspace", "index_pool_workspace",
@@ -276,9 +276,10 @@ def _calls():
     if _bind is None:
         import importlib.util
         import torch  # noqa: F401  (its libraries are loaded first)
-        if not os.path.exists(BIND):
-            raise ImportError(f"{BIND} is not built; run __graft_entry__.build() first")
-        spec = importlib.util.spec_from_file_location("_bind", BIND)
+        path = bind_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built; run __graft_entry__.build() first")
+        spec = importlib.util.spec_from_file_location("_bind", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         L = lib()

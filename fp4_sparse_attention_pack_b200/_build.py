@@ -1,5 +1,5 @@
-"""In-tree build of the CUDA library (libcsa2.so) for sm_100a with nvcc, and of the module with the Python
-calls of the paged key/value operators (_bind.so) with g++ against torch's headers."""
+"""In-tree build of the CUDA library (libcsa2.so) for sm_100a with nvcc, which needs nothing else, and, where torch
+is installed, of the module with the Python calls of the paged key/value operators with g++ against its headers."""
 from __future__ import annotations
 
 import glob
@@ -11,7 +11,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcsa2.so")
-BIND = os.path.join(PKG, "_bind.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -29,9 +28,15 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_path() -> str:
+    """The module with the Python calls: it serves the torch and the Python that it was built with."""
+    import torch
+    return os.path.join(PKG, f"_bind.{torch.__version__}.{sys.implementation.cache_tag}.so")
+
+
 def _build_bind(force: bool) -> None:
-    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "csa2.h")
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+    src, header, out = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "csa2.h"), bind_path()
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return
     import sysconfig
 
@@ -42,17 +47,21 @@ def _build_bind(force: bool) -> None:
             os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
     subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
                            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                           *[f"-I{d}" for d in dirs], src, "-o", BIND, f"-L{libs}", f"-Wl,-rpath,{libs}",
+                           *[f"-I{d}" for d in dirs], src, "-o", out, f"-L{libs}", f"-Wl,-rpath,{libs}",
                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    _build_bind(force)
     if force or _stale():
         cmd = ["nvcc", *ARCH, *FLAGS, *sources(), "-o", LIB]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.check_call(cmd)
+    try:
+        import torch  # noqa: F401
+    except ImportError:  # the C ABI alone
+        return LIB
+    _build_bind(force)
     return LIB
 
 
