@@ -299,11 +299,21 @@ def _want(t, what, dtype, shape, index=None):
     return at
 
 
+def _int32(**numbers) -> None:
+    """ctypes would keep the low bits only."""
+    for what, n in numbers.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{what} = {n} is out of range")
+
+
 def rotary(inv_freq, rot_dim: int, offset: int = 0, neighbours: bool = False, n_axes: int = 1, axis=None) -> csa2_rotary:
     """A rotation: channels offset .. offset + rot_dim - 1 of a head turn in pairs (neighbours, or half the
     rotation apart) by position * inv_freq[pair] (fp32 CUDA tensor).  axis (a list, one entry per pair) says
     which of the n_axes positions turns it."""
     import torch
+    _int32(rot_dim=rot_dim, offset=offset, n_axes=n_axes)
+    if axis is not None and not all(0 <= a < n_axes for a in axis):
+        raise ValueError(f"axis has entries outside 0 .. {n_axes - 1}")
     index = _want(inv_freq, "inv_freq", torch.float32, (rot_dim // 2,))
     r = csa2_rotary(inv_freq.data_ptr(), None, rot_dim, offset, int(neighbours), n_axes)
     if axis is not None:
@@ -356,6 +366,7 @@ def kv_append(cache: csa2_kv_cache, k, v, cu, max_new: int, start=None, rotary=N
 def kv_attn_workspace(cache: csa2_kv_cache, total: int, max_new: int, H: int) -> int:
     """Bytes of workspace for kv_attn calls of these sizes; what does for max_new does for fewer."""
     import torch
+    _int32(total=total, max_new=max_new, H=H)
     with torch.cuda.device(getattr(cache, "_index", -1)):
         return int(lib().csa2_kv_attn_workspace(ctypes.byref(cache), total, max_new, H))
 
