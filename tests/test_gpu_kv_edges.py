@@ -254,3 +254,29 @@ def test_small_channels_of_a_query_over_codes(csa, dtype, dim, H):
     bound = scale * dim * 2.0 ** -27 + 2.0 ** -21 * (1 + s.abs().amax(-1))
     d = (lse.double() - want).abs()
     assert (d <= bound).all(), (d / bound).max()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("old,new", [([1000, 300], [1, 2]), ([1000, 300], [30, 5]), ([1000, 300], [200, 140]), ([9000], [300])])
+def test_scores_that_are_all_minus_infinity(csa, dtype, cache, dim, old, new):
+    """Every score of a row is -infinity: zeros and lse -infinity (NaN over E4M3 pages in calls of at most 32 rows)."""
+    c = make(csa, old, new, 8, 2, dim, dtype, cache, seed=28)
+    c.hold_all()
+    n = old[0] + new[0]
+    at = torch.arange(n, device="cuda")
+    c.k_pages.permute(0, 2, 1, 3)[c.table[0, at // 64].long(), at % 64, :, 0] = torch.ones(n, 2, device="cuda").to(cache)
+    c.v_pages.permute(0, 2, 1, 3)[c.table[0, at // 64].long(), at % 64] = torch.full((n, 2, dim), 300.0, device="cuda").to(cache)
+    good, glse = c.attend(0.1)
+    c.q[0, 3, 0] = -math.inf
+    c.q[new[0] - 1, 6, 0] = -math.inf
+    out, lse = c.attend(0.1)
+    torch.cuda.synchronize()
+    keep = torch.ones(c.total, 8, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 3), (new[0] - 1, 6)):
+        if cache == E4 and max(new) * 4 <= 32:
+            assert out[t, h].isnan().all() and lse[t, h].isnan()
+        else:
+            assert (out[t, h] == 0).all() and torch.isneginf(lse[t, h])
+        keep[t, h] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
