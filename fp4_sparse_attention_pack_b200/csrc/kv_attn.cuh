@@ -1,5 +1,15 @@
-// What the two attention kernels over pages share: modes, conversions, the tensor
-// maps of the pools, and the join of partial results.
+// What the three attention kernels over pages share: modes, conversions, the tensor
+// maps of the pools, values that are not finite, and the join of partial results.
+//
+// Scores, exponentials, sums and outputs are fp32 until the output's one rounding, but
+// for the probabilities: the tensor cores multiply them with the values, so they are
+// rounded to the values' type (fp16 for E4M3; kv_codes.cu splits that in three).  The row
+// sum adds them unrounded, as lse needs it; the roundings of many keys average out.
+// Against 64 bits an output is off by 0.0023 of its size where its own rounding leaves
+// 0.0017 (bf16), 0.00028 and 0.00021 (fp16), 0.0017 both ways (E4M3).  A second bf16 term
+// for the rest of each probability took one token of 16 sequences to 32,768 from 205 to
+// 210 us and one over 1,000 from 14.8 to 15.6 us; in the chunk kernel it would be a
+// second product with V.
 #pragma once
 
 #include <cuda.h>
@@ -347,18 +357,17 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_
 
 }  // namespace
 
-// Calls of at most 16 rows to an item go to the few-rows kernel.  (One token of 8
-// sequences over 32,768, 64 / 8 heads of 128: 172 us there, 199 us in the chunk
-// kernel; heads of 64: 100 and 143 us.  Two tiles of 16 rows in it, 4 tokens each:
-// 348 us against 183 us in the chunk kernel.)
+// Calls of at most 16 rows to an item go to the few-rows kernel.  (8 sequences over
+// 32,768, 64 / 8 heads of 128: one token 169 us there, 178 us in the chunk kernel; two
+// 171 and 183 us; one token with heads of 64 97 and 126 us.  Two tiles of 16 rows in
+// it, 4 tokens each: 348 us against 181 us in the chunk kernel.)
 inline bool kv_few_rows(int max_new, int g) { return (int64_t)max_new * g <= 16; }
 
 // Calls over E4M3 pages with at most 32 rows to an item: the tensor cores read the
-// codes.  (8 sequences over 65,536, 64 / 8 heads of 128: one token 176 us against 229
-// us with codes widened in the few-rows kernel's registers, 4 tokens 215 against 393
-// us with codes widened in the chunk kernel's shared memory; heads of 64: 130 against
-// 162 and 193 against 303 us.  More rows would need more than 3 x 32 columns of each
-// product in TMEM.)
+// codes.  (8 sequences over 65,536, 64 / 8 heads of 128: one token 174 us against 386 us
+// in the chunk kernel, which widens codes in shared memory, 4 tokens 235 against 392 us;
+// heads of 64: 126 against 331 and 197 against 333 us.  More rows in this form would
+// need more than 3 x 32 columns of each product in TMEM.)
 inline bool kv_codes(int max_new, int g, int kv_dtype) {
     return kv_dtype == CSA2_KV_E4M3 && (int64_t)max_new * g <= 32;
 }

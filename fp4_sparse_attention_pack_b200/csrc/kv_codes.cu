@@ -30,9 +30,11 @@
 //   warp 10         loads and splits the queries and tells the others which item is next.
 //
 // The cache's bytes bound it: one token of 8 sequences over 65,536, 64 / 8 heads of
-// 128, takes 176 us (6.1 TB/s, 94% of the copy rate); with 32 rows (4 tokens each) the
-// softmax warps' instructions, some 470 a thread and block, bring it to 215 us (78%),
-// and heads of 64, whose blocks have half the bytes, to 130 and 193 us (64%, 43%).
+// 128, takes 174 us (6.2 TB/s, 96% of the copy rate).  With 32 rows (4 tokens each) it
+// takes 235 to 253 us by the machine (66 to 71%): no pipe is more than a third busy
+// (issue slots 33%), so it waits in the two groups' chains scores - split - product,
+// some 470 instructions a thread and block.  Heads of 64, whose blocks have half the
+// bytes and the same chain: 126 and 197 us (66%, 42%).
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

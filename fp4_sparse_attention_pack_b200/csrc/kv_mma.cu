@@ -33,11 +33,11 @@
 // (kv_attn.cuh); the pass that looks for it costs 12 prompts of up to 512 through a
 // window of 128 some 2 us of 31, other calls 1% or less.
 //
-// A chunk of 2,048 tokens over 16,384, 64 / 8 heads of 128, bf16: 1.05 ms (984
-// TFLOP/s, 58% of the burst rate, 69% of the sustained one).  A block takes 3,650
+// A chunk of 2,048 tokens over 16,384, 64 / 8 heads of 128, bf16: 1.06 ms (973
+// TFLOP/s, 57% of the burst rate, 69% of the sustained one).  A block takes 3,650
 // cycles for both tiles, of which the tensor pipe works 2,000: the chain scores ->
 // softmax (2,400) -> PV and the next scores (1,000) of a tile bounds it.  Chunks of up
-// to 1,024 over an E4M3 cache of 8,192: 341 us (755 TFLOP/s); there the widening warps
+// to 1,024 over an E4M3 cache of 8,192: 343 us (749 TFLOP/s); there the widening warps
 // share the issue slots.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -507,10 +507,11 @@ __device__ void role_load(Smem<kDim, kMode>& sm, const KvAttn& a, int g, Cursor 
 
 // ---------------------------------------------------------------- softmax
 
-// 2^t of two values in fp32 arithmetic, for t in [-126, 2^22): t = n + f with
-// |f| <= 1/2, a polynomial for 2^f (the minimax one of degree 4, computed for
-// this file by Remez exchange: relative error 2.6e-6, far below the rounding to
-// 16 bits) times 2^n.  Below -126 the value is that of -126; NaN stays NaN.
+// 2^t of two values in fp32 arithmetic, for t in [-126, 127.5) (its callers' are at most
+// kGap + 7 = 15): t = n + f with |f| <= 1/2, a polynomial for 2^f (the minimax one of
+// degree 4, computed for this file by Remez exchange: relative error 2.6e-6, far below
+// the rounding to 16 bits) times 2^n.  Below -126 the value is that of -126; NaN stays
+// NaN.
 __device__ __forceinline__ float2 ex2_poly(float2 t) {
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.x) : "f"(-126.0f));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(t.y) : "f"(-126.0f));

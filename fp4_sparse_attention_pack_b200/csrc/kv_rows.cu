@@ -16,8 +16,8 @@
 // The work is cut evenly over the CTAs (kv_plan.cuh), which splits long
 // sequences when there are few.
 //
-// One token of 16 sequences to 32,768, 64 / 8 heads of 128, bf16: 209 us (6.3 TB/s,
-// 98% of the copy rate); heads of 64: 83%.
+// One token of 16 sequences to 32,768, 64 / 8 heads of 128, bf16: 205 to 211 us by the
+// machine (6.2 to 6.4 TB/s, 97% of the copy rate and more); heads of 64: 85%.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
