@@ -33,11 +33,11 @@
 // (kv_attn.cuh); the pass that looks for it costs 12 prompts of up to 512 through a
 // window of 128 some 2 us of 31, other calls 1% or less.
 //
-// A chunk of 2,048 tokens over 16,384, 64 / 8 heads of 128, bf16: 1.06 ms (973
-// TFLOP/s, 57% of the burst rate, 69% of the sustained one).  A block takes 3,650
+// A chunk of 2,048 tokens over 16,384, 64 / 8 heads of 128, bf16: 1.06 to 1.08 ms
+// by the machine (973 TFLOP/s, 57% of the burst rate, 69% of the sustained one).  A block takes 3,650
 // cycles for both tiles, of which the tensor pipe works 2,000: the chain scores ->
 // softmax (2,400) -> PV and the next scores (1,000) of a tile bounds it.  Chunks of up
-// to 1,024 over an E4M3 cache of 8,192: 343 us (749 TFLOP/s); there the widening warps
+// to 1,024 over an E4M3 cache of 8,192: 341 to 346 us (749 TFLOP/s); there the widening warps
 // share the issue slots.
 #include <cuda.h>
 #include <cudaTypedefs.h>

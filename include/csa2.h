@@ -558,7 +558,8 @@ int csa2_rotate(const csa2_rotary* rot, const csa2_heads* x, const csa2_heads* y
  * value (ties to even, saturating at +-448), without a scale, like the FP8
  * window.  `status` collects CSA2_DEVERR_* bits.  Rows of a page behind
  * n_tokens may hold anything, NaN included: they never reach a result.  A key and
- * its value reach only the tokens that see the key, NaN and infinities too.
+ * its value reach only the tokens that see the key, NaN and infinities too (an
+ * infinite value whose probability rounds to 0 gives NaN).
  */
 #define CSA2_KV_BF16 0
 #define CSA2_KV_F16 1
@@ -585,7 +586,8 @@ typedef struct {
  * at and behind cu[batch] are neither read nor written).  A sequence may bring
  * none.  max_new is a bound that the caller knows: no sequence brings more.  A
  * sequence whose bounds break these rules sets CSA2_DEVERR_COUNT and is left
- * out whole.
+ * out whole; the others are not affected (a row that bounds out of order give to
+ * two of them is appended to both, and gets the attention of either).
  *
  * csa2_kv_append writes the i-th new token of sequence b to slot start[b] + i
  * and sets n_tokens[b] = start[b] + (its new tokens).  start is device int32
